@@ -492,6 +492,162 @@ int wan_attention_fp8_fwd(const wan_dit_config* cfg, const void* q, int64_t q_ro
 /* Bytes of the wan_attention_fp8_fwd workspace for B samples, Lq queries, Lk keys. */
 size_t wan_attention_fp8_workspace_bytes(const wan_dit_config* cfg, int B, int Lq, int Lk);
 
+/* ---- packed documents --------------------------------------------------------------- */
+
+/* A packed tensor holds documents (clips, images, texts) of different lengths one after
+ * another along its row axis: document d of n_docs owns rows [cu[d], cu[d+1]) of a
+ * DEVICE array cu of n_docs + 1 int32, 0 <= cu[0] <= cu[1] <= ... <= the tensor's rows
+ * (offsets outside that order are clamped into it, so they cannot reach past the
+ * tensor). A document may be empty. Rows in front of cu[0] and from cu[n_docs] on belong
+ * to no document: the calls neither use their values nor write their results. The Wan 2.1
+ * pages have no counterpart of these calls (their batches share one length, and the pages
+ * name neither positions nor a q/k norm); they are the parts that a model with them, or a
+ * batch of clips of mixed sizes, needs beside wan_adaln_modulate, wan_linear_fwd and
+ * wan_attention_fwd, with their gradients. Tensors of one call must not overlap unless a
+ * call says so. Offsets are 64-bit: a tensor may exceed 2^31 elements; row counts are int.
+ * All results are the same from run to run (no atomics on floating-point values). */
+
+/* Rows of a tensor: row r starts at ptr + r * row_stride elements. ptr is 16-byte
+ * aligned; row_stride >= the row's width. */
+typedef struct {
+  void* ptr;
+  int64_t row_stride;
+} wan_rows;
+
+/* Rotary positions. The first axis_dim[0] + ... + axis_dim[n_axes-1] = R dims of every
+ * head are rotated, the others pass. R is even and <= head_dim, and so are its parts
+ * (axis_dim[a] >= 2). Pair p < R/2 belongs to axis a when it lies in a's part of the
+ * pairs (axis_dim[a]/2 of them); as pair i of that part it turns by
+ * positions[row, a] * f, f = theta^(-2i/axis_dim[a]) before scaling. A pair (x, y) goes to
+ * amplitude * (x cos - y sin, x sin + y cos). */
+typedef enum {
+  WAN_ROPE_INTERLEAVED = 0, /* pair p is dims (2p, 2p+1)     */
+  WAN_ROPE_HALF = 1         /* pair p is dims (p, p + R/2)   */
+} wan_rope_layout;
+typedef enum {
+  WAN_ROPE_SCALE_NONE = 0,
+  WAN_ROPE_SCALE_LINEAR = 1, /* f / factor                                                   */
+  WAN_ROPE_SCALE_BASE = 2,   /* theta * factor^(n/(n-2)), n = axis_dim[a] > 2                */
+  WAN_ROPE_SCALE_RAMP = 3    /* t = orig_len f / 2 pi turns over the original length:        */
+                             /* f * (w + (1-w)/factor), w = clamp((t - slow)/(fast - slow))  */
+} wan_rope_scaling;
+typedef struct {
+  int layout;          /* wan_rope_layout                                */
+  int scaling;         /* wan_rope_scaling, of every axis                */
+  int n_axes;          /* 1..3                                           */
+  int axis_dim[3];
+  int orig_len[3];     /* RAMP: positions the model was trained on, > 0  */
+  double theta;        /* > 1                                            */
+  double factor[3];    /* scaling != NONE: > 0 per axis                  */
+  double fast, slow;   /* RAMP: fast > slow                              */
+  double amplitude;    /* finite, not 0                                  */
+} wan_rope;
+typedef enum {
+  WAN_QK_NORM_NONE = 0,
+  WAN_QK_NORM_HEAD = 1,  /* x / sqrt(mean(x^2) + eps) * w over each head, w [head_dim]                */
+  WAN_QK_NORM_WIDTH = 2  /* the same over the whole width, w_q [heads*head_dim], w_k [kv_heads*head_dim] */
+} wan_qk_norm;
+
+/* Norm of q and k, then the rotation, before attention. q [rows, heads*head_dim], k
+ * [rows, kv_heads*head_dim] act (e.g. columns of a fused projection); k and k_out NULL: q
+ * alone. positions [rows, n_axes] int32 (any sign; angles are reduced in 64 bits). w_q,
+ * w_k act (norm != NONE). The outputs may be the inputs themselves. head_dim <= 128,
+ * even; heads + kv_heads <= 96 (WAN_ERR_UNSUPPORTED else); kv_heads >= 1. Statistics in fp32. */
+int wan_qk_norm_rope_fwd(const wan_dit_config* cfg, const wan_rope* rope, const int32_t* positions, int rows,
+                         int kv_heads, int norm, const wan_rows* q, const wan_rows* k, const void* w_q,
+                         const void* w_k, const wan_rows* q_out, const wan_rows* k_out, void* stream);
+
+/* Its gradient: dq_out, dk_out act (gradients of q_out, k_out); q, k the call's INPUTS
+ * (only read with a norm; NULL allowed for WAN_QK_NORM_NONE) -> dq, dk act, and, with a norm,
+ * dw_q, dw_k fp32 in the shape of w_q, w_k (either may be NULL). dq may be dq_out. The
+ * workspace is wan_qk_norm_rope_workspace_bytes (0 bytes, NULL, for WAN_QK_NORM_NONE). */
+int wan_qk_norm_rope_bwd(const wan_dit_config* cfg, const wan_rope* rope, const int32_t* positions, int rows,
+                         int kv_heads, int norm, const wan_rows* dq_out, const wan_rows* dk_out, const wan_rows* q,
+                         const wan_rows* k, const void* w_q, const void* w_k, const wan_rows* dq, const wan_rows* dk,
+                         float* dw_q, float* dw_k, void* workspace, size_t ws_bytes, void* stream);
+size_t wan_qk_norm_rope_workspace_bytes(const wan_dit_config* cfg, int rows, int kv_heads, int norm);
+
+/* The residual step between two branches of a block, for documents that each have their
+ * own modulation:
+ *   x_out = residual_scale * x + gate_d * (norm_post(y) * w_post)
+ *   h     = (norm_pre(x_out) * w_pre + b_pre) * (1 + scale_d) + shift_d
+ * with gate_d = e[d, gate] + mod_bias[gate] (1 for gate = -1) and, as in
+ * wan_adaln_modulate, shift_d = e[d, 3 chunk] + mod_bias[3 chunk], scale_d = e[d, 3 chunk + 1]
+ * + mod_bias[3 chunk + 1] (chunk = -1: no modulation). Norms over the width, eps of the
+ * config: LAYER subtracts the mean and divides by sqrt(var + eps), RMS divides by
+ * sqrt(mean(x^2) + eps). Absent weights are 1, absent biases 0. */
+typedef enum { WAN_NORM_NONE = 0, WAN_NORM_LAYER = 1, WAN_NORM_RMS = 2 } wan_norm_kind;
+typedef struct {
+  int pre;               /* LAYER or RMS                              */
+  int post;              /* wan_norm_kind                             */
+  int gate;              /* -1..5                                     */
+  int chunk;             /* -1..1                                     */
+  float residual_scale;
+  const void *w_pre, *b_pre; /* [D] act or NULL                       */
+  const void* w_post;    /* [D] act or NULL (NULL for post = NONE)    */
+} wan_residual_norm;
+
+/* x [rows, D] fp32, y [rows, D] act, e [n_docs, 6, D] fp32 (may be NULL with gate = chunk =
+ * -1), mod_bias [6, D] fp32 or NULL -> x_out [rows, D] fp32 (may be x), h_out [rows, D] act
+ * (may be y). D <= 8192. */
+int wan_gated_residual_norm_fwd(const wan_dit_config* cfg, const wan_residual_norm* op, const float* x, const void* y,
+                                const float* e, const float* mod_bias, const int32_t* cu_rows, int n_docs, int rows,
+                                float* x_out, void* h_out, void* stream);
+
+/* Its gradient. x_out: the forward's result; y its branch input; dh [rows, D] act the
+ * gradient of h, dx_out [rows, D] fp32 the one that reaches x_out from later steps (NULL: 0).
+ * -> dx [rows, D] fp32 (of x; may be dx_out), dy [rows, D] act (may be dh), and, each unless
+ * NULL: de [n_docs, 6, D] fp32, of which only the rows gate, 3 chunk and 3 chunk + 1 of every
+ * document are written (0 for an empty one); dmod_bias [6, D] fp32, the same rows; dw_pre,
+ * db_pre, dw_post [D] fp32 (sums over all documents; of absent weights too). */
+typedef struct {
+  float *de, *dmod_bias, *dw_pre, *db_pre, *dw_post;
+} wan_residual_norm_grads;
+int wan_gated_residual_norm_bwd(const wan_dit_config* cfg, const wan_residual_norm* op, const float* x_out,
+                                const void* y, const float* e, const float* mod_bias, const int32_t* cu_rows,
+                                int n_docs, int rows, const void* dh, const float* dx_out, float* dx, void* dy,
+                                const wan_residual_norm_grads* grads, void* workspace, size_t ws_bytes, void* stream);
+size_t wan_gated_residual_norm_workspace_bytes(const wan_dit_config* cfg, int rows, int n_docs);
+
+/* Attention inside documents: query row i (of Lq, from 0) of document d sees keys
+ * [0, n_i) of the same document's Lk keys,
+ *   n_i = Lk                                                          causal_block = 0
+ *   n_i = max(min(prefix_d, Lk), min(Lk, (floor((i + Lk - Lq) / g) + 1) g))   g = causal_block > 0
+ * (at least 0): with g = 1 the ordinary causal order, aligned at the documents' ends, with g
+ * tokens per frame the order of frames; the first prefix_d keys are seen by every query.
+ * Scores are s = cap tanh(scale q.k / cap) - slope_h |i + Lk - Lq - j| (cap = 0: no cap;
+ * slopes NULL: 0). A query that sees no key has output 0 and log-sum -infinity. Query
+ * head h reads key head h / (heads / kv_heads). */
+typedef struct {
+  int n_docs;
+  const int32_t *cu_q, *cu_k;  /* device [n_docs + 1]               */
+  const int32_t* prefix;       /* device [n_docs] (>= 0) or NULL: 0 */
+  int causal_block;            /* >= 0                              */
+  float scale;                 /* finite; 0: 1/sqrt(head_dim)       */
+  float cap;                   /* finite, >= 0                      */
+  const float* slopes;         /* device [heads] fp32 or NULL       */
+} wan_documents;
+
+/* q [q_rows, heads*head_dim], k and v [k_rows, kv_heads*head_dim] act -> o [q_rows,
+ * heads*head_dim] act and, unless NULL, lse [heads, q_rows] fp32 (natural log of the sum of
+ * e^s). kv_heads divides heads. Values of a document's own rows must be finite. The
+ * workspace lets few query rows over many keys be split over the keys; it may be NULL
+ * (0 bytes), which never splits. */
+int wan_attention_packed_fwd(const wan_dit_config* cfg, const wan_documents* docs, int q_rows, int k_rows,
+                             int kv_heads, const wan_rows* q, const wan_rows* k, const wan_rows* v, const wan_rows* o,
+                             float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+/* Its gradient from o and lse of the forward: do act -> dq, dk, dv act (each required).
+ * Keys that no query sees get 0. Workspace required. */
+int wan_attention_packed_bwd(const wan_dit_config* cfg, const wan_documents* docs, int q_rows, int k_rows,
+                             int kv_heads, const wan_rows* q, const wan_rows* k, const wan_rows* v, const wan_rows* o,
+                             const float* lse, const wan_rows* d_o, const wan_rows* dq, const wan_rows* dk,
+                             const wan_rows* dv, void* workspace, size_t ws_bytes, void* stream);
+/* Bytes of the forward's (backward = 0) or the gradient's (1) workspace; one buffer of the
+ * larger size serves both in turn. 0 on a bad config. */
+size_t wan_attention_packed_workspace_bytes(const wan_dit_config* cfg, int q_rows, int k_rows, int n_docs,
+                                            int kv_heads, int backward);
+
 /* ---- tracing ------------------------------------------------------------------- */
 
 /* Total number of kernels this library has launched in this process. */

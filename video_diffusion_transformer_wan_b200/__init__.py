@@ -134,6 +134,7 @@ def _load() -> ctypes.CDLL:
         "wan_trace_read": (_i, [_i, P(ctypes.c_double), P(_i64)]),
         "wan_trace_launches": (_i, [_i, P(_i), P(ctypes.c_double), P(ctypes.c_double)]),
     }
+    sig.update(packed.signatures())
     for name, (res, args) in sig.items():
         f = getattr(L, name)
         f.restype = res
@@ -490,3 +491,9 @@ def trace_read(kind: int):
     n = ctypes.c_int64()
     _check(_lib().wan_trace_read(kind, ctypes.byref(ms), ctypes.byref(n)), "wan_trace_read")
     return ms.value, n.value
+
+
+from . import packed  # noqa: E402  (needs the names above)
+from .packed import *  # noqa: E402,F401,F403
+
+__all__ += packed.__all__

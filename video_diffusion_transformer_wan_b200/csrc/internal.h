@@ -158,6 +158,26 @@ int launch_attn_tc_fp8(const void* q_codes, const float* q_scale, const void* k_
 int launch_attn_simt(AttnOperand q, AttnOperand k, AttnOperand v, void* o, int64_t o_row_stride, int o_col0,
                      int B, int H, int Lq, int Lk, int d, cudaStream_t s);
 
+// Attention inside packed documents (wan_attention_packed_*), scores and masks as in
+// wan_documents. o and the gradients are written for documents' rows only.
+struct PackedAttn {
+  const int32_t *cu_q, *cu_k, *prefix;
+  const float* slopes;
+  int n_docs, q_rows, k_rows, H, Hk, d, causal_block;
+  float scale, cap;
+  const void *q, *k, *v;
+  void* o;
+  float* lse;             // [H, q_rows] or NULL (forward)
+  int64_t q_stride, k_stride, v_stride, o_stride;
+  const void* d_o;        // gradient
+  void *dq, *dk, *dv;
+  int64_t do_stride, dq_stride, dk_stride, dv_stride;
+  float* delta;           // gradient: [H, q_rows], row sums of do * o
+};
+// CUDA cores, fp32 arithmetic, head_dim <= 128 (act = dtype).
+int launch_attn_packed_simt(const PackedAttn& p, int dtype, cudaStream_t s);
+int launch_attn_packed_simt_bwd(const PackedAttn& p, int dtype, cudaStream_t s);
+
 // Small kernels.
 int launch_patch_gather(const void* latent, int B, int C, int F, int H, int W, void* patches, int dtype,
                         cudaStream_t s);

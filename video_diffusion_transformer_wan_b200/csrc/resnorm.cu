@@ -1,0 +1,588 @@
+// The residual step between two branches, with the norms around it, for packed documents
+// (wan_gated_residual_norm_*):
+//   x' = a x + gate_d post(y) w_post,   h = (pre(x') w + b)(1 + scale_d) + shift_d.
+//
+// Gradient, with G = dx_out + (d h / d x')^T dh: dn = dh (1 + scale_d) w;
+// d x' = G = dx_out + r (dn - [mean(dn)] - n mean(dn n)) (the bracket for LAYER only);
+// dx = a G; the branch gets dyn = G gate_d w_post and dy through its own norm. Everything
+// that is summed over rows follows from three sums per document and column:
+//   S0 = sum dh, S1 = sum dh n, S2 = sum G yn:   dshift = S0, dscale = w S1 + b S0,
+//   dgate = w_post S2, dw = sum_d (1 + scale_d) S1, db = sum_d (1 + scale_d) S0,
+//   dw_post = sum_d gate_d S2.
+//
+// HBM-bound: 4 + es bytes in, 4 + es out per element (es = 2 or 4), the gradient 8 + 2 es
+// in. A block owns one row at a time in registers, 8 columns per thread and unit, and walks a
+// contiguous range of rows, so the per-document vectors (folded to three) and, in the
+// gradient, the three column sums stay in registers until the document changes. Sums leave
+// as partial rows, one per (block, document) that meet, at slot block + document (both only
+// grow along the rows, so slots never collide), and are added in order by a second kernel:
+// no atomics. All statistics are fp32 in two passes over the registers.
+#include <cuda_bf16.h>
+
+#include "checks.h"
+#include "internal.h"
+#include "packed.cuh"
+
+namespace wan {
+namespace {
+
+constexpr int kMaxBlocks = 148 * 8;
+
+struct ResNormParams {
+  const float* x;      // forward: x; gradient: x_out of the forward
+  const void* y;
+  const float *e, *mod_bias;
+  const int32_t* cu;
+  int n_docs, rows, D;
+  int pre, post, gate, chunk;
+  float residual_scale, eps;
+  const void *w_pre, *b_pre, *w_post;
+  float* x_out;
+  void* h_out;
+  const void* dh;      // gradient
+  const float* dx_out;
+  float* dx;
+  void* dy;
+  float* part;         // [slot][3][D]
+};
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Sums of K values over the block, the same in every thread and run. `buf` alternates
+// between two halves, so that one barrier per call is enough.
+template <int K>
+__device__ __forceinline__ void block_sums(float (&v)[K], float (&buf)[2][32][2], int& half) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = warp_sum(v[k]);
+  const int warps = blockDim.x >> 5;
+  if (warps == 1) return;
+  if ((threadIdx.x & 31) == 0)
+#pragma unroll
+    for (int k = 0; k < K; ++k) buf[half][threadIdx.x >> 5][k] = v[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    float s = 0.f;
+    for (int w = 0; w < warps; ++w) s += buf[half][w][k];
+    v[k] = s;
+  }
+  half ^= 1;
+}
+
+// Document of `row` (the last one that begins at or before it and is not empty there), by
+// bisection; row lies in [cu[0], cu[n_docs]).
+__device__ __forceinline__ int doc_of_row(const int32_t* cu, int n_docs, int row) {
+  int lo = 0, hi = n_docs;  // cu[lo] <= row < cu[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(cu + mid) <= row) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Rows [lo, hi) of the documents and this block's share of them, cut evenly.
+struct RowSpan {
+  int64_t lo, hi;
+};
+__device__ __forceinline__ RowSpan block_rows(const ResNormParams& p, int block, int blocks) {
+  const int64_t a = min(max(__ldg(p.cu), 0), p.rows);
+  const int64_t b = min(max(__ldg(p.cu + p.n_docs), static_cast<int>(a)), p.rows);
+  const int64_t n = b - a;
+  return {a + n * block / blocks, a + n * (block + 1) / blocks};
+}
+
+template <typename T>
+__device__ __forceinline__ float at(const void* w, int i, float absent) {
+  return w ? to_f32<T>(static_cast<const T*>(w)[i]) : absent;
+}
+__device__ __forceinline__ float mod_at(const ResNormParams& p, int doc, int which, int col) {
+  float v = __ldg(p.e + (static_cast<int64_t>(doc) * 6 + which) * p.D + col);
+  if (p.mod_bias) v += __ldg(p.mod_bias + static_cast<int64_t>(which) * p.D + col);
+  return v;
+}
+
+// v -> (v - mean) r (LAYER) or v r (RMS), in place; returns r.
+template <int NU>
+__device__ __forceinline__ float normalise(float (&v)[NU][8], const bool (&on)[NU], int kind, float inv_d, float eps,
+                                           float (&buf)[2][32][2], int& half) {
+  if (kind == WAN_NORM_LAYER) {
+    float s[1] = {0.f};
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[0] += v[u][i];  // absent units hold zeros
+    block_sums<1>(s, buf, half);
+    const float mean = s[0] * inv_d;
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[u][i] = on[u] ? v[u][i] - mean : 0.f;
+  }
+  float q[1] = {0.f};
+#pragma unroll
+  for (int u = 0; u < NU; ++u)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[0] += v[u][i] * v[u][i];
+  block_sums<1>(q, buf, half);
+  const float r = 1.0f / sqrtf(q[0] * inv_d + eps);
+#pragma unroll
+  for (int u = 0; u < NU; ++u)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[u][i] *= r;
+  return r;
+}
+
+template <typename T, int NU, int kMaxThreads>
+__global__ void __launch_bounds__(kMaxThreads) gated_residual_norm_kernel(const ResNormParams p) {
+  __shared__ float buf[2][32][2];
+  int half = 0;
+  const int tpr = blockDim.x;
+  int col[NU];
+  bool on[NU];
+#pragma unroll
+  for (int u = 0; u < NU; ++u) {
+    col[u] = (u * tpr + threadIdx.x) * 8;
+    on[u] = col[u] < p.D;
+  }
+  const float inv_d = 1.0f / static_cast<float>(p.D);
+  const RowSpan span = block_rows(p, blockIdx.x, gridDim.x);
+  if (span.lo >= span.hi) return;
+  float g[NU][8], sc[NU][8], sh[NU][8];  // gate w_post; w (1 + scale); b (1 + scale) + shift
+  int64_t doc_end = -1;
+  Raw8<float> rx[NU];
+  Raw8<T> ry[NU];
+  auto load = [&](int64_t row) {
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+      if (on[u]) {
+        load_raw8(rx[u], p.x + row * p.D + col[u]);
+        load_raw8(ry[u], static_cast<const T*>(p.y) + row * p.D + col[u]);
+      }
+  };
+  load(span.lo);
+  for (int64_t row = span.lo; row < span.hi; ++row) {
+    if (row >= doc_end) {
+      const int doc = doc_of_row(p.cu, p.n_docs, static_cast<int>(row));
+      doc_end = max(__ldg(p.cu + doc + 1), static_cast<int>(row) + 1);
+#pragma unroll
+      for (int u = 0; u < NU; ++u)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int c = col[u] + i;
+          if (!on[u]) continue;
+          g[u][i] = at<T>(p.w_post, c, 1.f) * (p.gate >= 0 ? mod_at(p, doc, p.gate, c) : 1.f);
+          const float s1 = p.chunk >= 0 ? 1.f + mod_at(p, doc, 3 * p.chunk + 1, c) : 1.f;
+          sc[u][i] = at<T>(p.w_pre, c, 1.f) * s1;
+          sh[u][i] = at<T>(p.b_pre, c, 0.f) * s1 + (p.chunk >= 0 ? mod_at(p, doc, 3 * p.chunk, c) : 0.f);
+        }
+    }
+    float x[NU][8], y[NU][8];
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      if (on[u]) {
+        unpack8(rx[u], x[u]);
+        unpack8(ry[u], y[u]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[u][i] = y[u][i] = 0.f;
+      }
+    }
+    if (row + 1 < span.hi) load(row + 1);  // in flight while this row's sums are formed
+    if (p.post != WAN_NORM_NONE) normalise<NU>(y, on, p.post, inv_d, p.eps, buf, half);
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+      if (on[u]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[u][i] = fmaf(y[u][i], g[u][i], p.residual_scale * x[u][i]);
+        store_vec8(p.x_out + row * p.D + col[u], x[u]);
+      }
+    normalise<NU>(x, on, p.pre, inv_d, p.eps, buf, half);
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+      if (on[u]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[u][i] = fmaf(x[u][i], sc[u][i], sh[u][i]);
+        store_vec8(static_cast<T*>(p.h_out) + row * p.D + col[u], x[u]);
+      }
+  }
+}
+
+template <typename T, int NU, int kMaxThreads>
+__global__ void __launch_bounds__(kMaxThreads) gated_residual_norm_bwd_kernel(const ResNormParams p) {
+  __shared__ float buf[2][32][2];
+  int half = 0;
+  const int tpr = blockDim.x;
+  int col[NU];
+  bool on[NU];
+#pragma unroll
+  for (int u = 0; u < NU; ++u) {
+    col[u] = (u * tpr + threadIdx.x) * 8;
+    on[u] = col[u] < p.D;
+  }
+  const float inv_d = 1.0f / static_cast<float>(p.D);
+  const RowSpan span = block_rows(p, blockIdx.x, gridDim.x);
+  if (span.lo >= span.hi) return;
+  float g[NU][8], sc[NU][8];                      // gate w_post; w (1 + scale)
+  float s0[NU][8] = {}, s1[NU][8] = {}, s2[NU][8] = {};
+  int doc = -1;
+  int64_t doc_end = -1;
+  auto flush = [&]() {
+    if (!p.part) return;
+    float* out = p.part + (static_cast<int64_t>(blockIdx.x) + doc) * 3 * p.D;
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      if (on[u]) {
+        store_vec8(out + col[u], s0[u]);
+        store_vec8(out + p.D + col[u], s1[u]);
+        store_vec8(out + 2 * static_cast<int64_t>(p.D) + col[u], s2[u]);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s0[u][i] = s1[u][i] = s2[u][i] = 0.f;
+    }
+  };
+  for (int64_t row = span.lo; row < span.hi; ++row) {
+    float n[NU][8], y[NU][8], dh[NU][8], G[NU][8];
+    {
+      Raw8<float> rn[NU], rg[NU];
+      Raw8<T> ry[NU], rh[NU];
+#pragma unroll
+      for (int u = 0; u < NU; ++u)
+        if (on[u]) {
+          load_raw8(rn[u], p.x + row * p.D + col[u]);
+          load_raw8(rh[u], static_cast<const T*>(p.dh) + row * p.D + col[u]);
+          load_raw8(ry[u], static_cast<const T*>(p.y) + row * p.D + col[u]);
+          if (p.dx_out) load_raw8(rg[u], p.dx_out + row * p.D + col[u]);
+        }
+      if (row >= doc_end) {
+        if (doc >= 0) flush();
+        doc = doc_of_row(p.cu, p.n_docs, static_cast<int>(row));
+        doc_end = max(__ldg(p.cu + doc + 1), static_cast<int>(row) + 1);
+#pragma unroll
+        for (int u = 0; u < NU; ++u)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int c = col[u] + i;
+            if (!on[u]) continue;
+            g[u][i] = at<T>(p.w_post, c, 1.f) * (p.gate >= 0 ? mod_at(p, doc, p.gate, c) : 1.f);
+            sc[u][i] = at<T>(p.w_pre, c, 1.f) * (p.chunk >= 0 ? 1.f + mod_at(p, doc, 3 * p.chunk + 1, c) : 1.f);
+          }
+      }
+#pragma unroll
+      for (int u = 0; u < NU; ++u) {
+        if (on[u]) {
+          unpack8(rn[u], n[u]);
+          unpack8(rh[u], dh[u]);
+          unpack8(ry[u], y[u]);
+          if (p.dx_out) unpack8(rg[u], G[u]);
+        }
+        if (!on[u] || !p.dx_out)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            G[u][i] = 0.f;
+            if (!on[u]) n[u][i] = dh[u][i] = y[u][i] = 0.f;
+          }
+      }
+    }
+    const float r = normalise<NU>(n, on, p.pre, inv_d, p.eps, buf, half);
+    float m[2] = {0.f, 0.f};  // sums of dn n and dn
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+      if (on[u])
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          s0[u][i] += dh[u][i];
+          s1[u][i] = fmaf(dh[u][i], n[u][i], s1[u][i]);
+          dh[u][i] *= sc[u][i];
+          m[0] = fmaf(dh[u][i], n[u][i], m[0]);
+          m[1] += dh[u][i];
+        }
+    block_sums<2>(m, buf, half);
+    const float a = m[0] * inv_d, c = p.pre == WAN_NORM_LAYER ? m[1] * inv_d : 0.f;
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+      if (on[u]) {
+        float dx[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          G[u][i] = fmaf(r, dh[u][i] - c - n[u][i] * a, G[u][i]);
+          dx[i] = p.residual_scale * G[u][i];
+        }
+        store_vec8(p.dx + row * p.D + col[u], dx);
+      }
+    if (p.post == WAN_NORM_NONE) {
+#pragma unroll
+      for (int u = 0; u < NU; ++u)
+        if (on[u]) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            s2[u][i] = fmaf(G[u][i], y[u][i], s2[u][i]);
+            y[u][i] = G[u][i] * g[u][i];
+          }
+          store_vec8(static_cast<T*>(p.dy) + row * p.D + col[u], y[u]);
+        }
+    } else {
+      const float ry = normalise<NU>(y, on, p.post, inv_d, p.eps, buf, half);
+      float k[2] = {0.f, 0.f};
+#pragma unroll
+      for (int u = 0; u < NU; ++u)
+        if (on[u])
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            s2[u][i] = fmaf(G[u][i], y[u][i], s2[u][i]);
+            G[u][i] *= g[u][i];
+            k[0] = fmaf(G[u][i], y[u][i], k[0]);
+            k[1] += G[u][i];
+          }
+      block_sums<2>(k, buf, half);
+      const float ka = k[0] * inv_d, kc = p.post == WAN_NORM_LAYER ? k[1] * inv_d : 0.f;
+#pragma unroll
+      for (int u = 0; u < NU; ++u)
+        if (on[u]) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[u][i] = ry * (G[u][i] - kc - y[u][i] * ka);
+          store_vec8(static_cast<T*>(p.dy) + row * p.D + col[u], y[u]);
+        }
+    }
+  }
+  flush();
+}
+
+// Sums over a document's rows: slots block + doc of the blocks whose span meets the
+// document, in order (thread row y takes every 8th). Writes S0..S2 to `total` and, when
+// asked, the document's rows of de.
+template <typename T>
+__global__ void __launch_bounds__(256) resnorm_doc_sums_kernel(const ResNormParams p, int blocks, float* total, float* de) {
+  __shared__ float acc[3][8][33];
+  const int c = blockIdx.x * 32 + threadIdx.x;
+  for (int doc = blockIdx.y; doc < p.n_docs; doc += gridDim.y) {
+    const int64_t a = min(max(__ldg(p.cu), 0), p.rows);
+    const int64_t b = min(max(__ldg(p.cu + p.n_docs), static_cast<int>(a)), p.rows);
+    const DocRange dr = doc_range(p.cu, doc, p.rows);
+    float s[3] = {0.f, 0.f, 0.f};
+    const int64_t n = b - a;
+    if (dr.count > 0 && dr.first >= a && n > 0 && c < p.D) {
+      // block k holds rows [a + n k / B, a + n (k + 1) / B)
+      const int k0 = static_cast<int>(((dr.first - a + 1) * blocks - 1) / n);
+      const int k1 = static_cast<int>(min((dr.first - a + dr.count) * blocks - 1, n * blocks - 1) / n);
+      for (int k = k0 + threadIdx.y; k <= k1; k += 8) {
+        const float* row = p.part + (static_cast<int64_t>(k) + doc) * 3 * p.D + c;
+        // a block without rows of its own lies between two cuts at one place
+        if (a + n * k / blocks < a + n * (k + 1) / blocks)
+#pragma unroll
+          for (int q = 0; q < 3; ++q) s[q] += row[static_cast<int64_t>(q) * p.D];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 3; ++q) acc[q][threadIdx.y][threadIdx.x] = s[q];
+    __syncthreads();
+    if (threadIdx.y < 3 && c < p.D) {
+      float v = 0.f;
+#pragma unroll
+      for (int y = 0; y < 8; ++y) v += acc[threadIdx.y][y][threadIdx.x];
+      acc[threadIdx.y][0][threadIdx.x] = v;
+      total[(static_cast<int64_t>(doc) * 3 + threadIdx.y) * p.D + c] = v;
+    }
+    __syncthreads();
+    if (threadIdx.y == 0 && de && c < p.D) {
+      float* out = de + static_cast<int64_t>(doc) * 6 * p.D + c;
+      const float S0 = acc[0][0][threadIdx.x], S1 = acc[1][0][threadIdx.x], S2 = acc[2][0][threadIdx.x];
+      if (p.chunk >= 0) {
+        out[static_cast<int64_t>(3 * p.chunk) * p.D] = S0;
+        out[static_cast<int64_t>(3 * p.chunk + 1) * p.D] = at<T>(p.w_pre, c, 1.f) * S1 + at<T>(p.b_pre, c, 0.f) * S0;
+      }
+      if (p.gate >= 0) out[static_cast<int64_t>(p.gate) * p.D] = at<T>(p.w_post, c, 1.f) * S2;
+    }
+  }
+}
+
+// Sums over documents, in order: the gradients of the weights and of mod_bias.
+template <typename T>
+__global__ void __launch_bounds__(128) resnorm_weight_sums_kernel(const ResNormParams p, const float* total,
+                                                                  wan_residual_norm_grads out) {
+  const int c = blockIdx.x * 128 + threadIdx.x;
+  if (c >= p.D) return;
+  float dw = 0.f, db = 0.f, dwp = 0.f, m0 = 0.f, m1 = 0.f, m2 = 0.f;
+  const float w = at<T>(p.w_pre, c, 1.f), b = at<T>(p.b_pre, c, 0.f), wp = at<T>(p.w_post, c, 1.f);
+  for (int doc = 0; doc < p.n_docs; ++doc) {
+    const float* t = total + static_cast<int64_t>(doc) * 3 * p.D + c;
+    const float S0 = t[0], S1 = t[p.D], S2 = t[2 * static_cast<int64_t>(p.D)];
+    const float s1 = p.chunk >= 0 ? 1.f + mod_at(p, doc, 3 * p.chunk + 1, c) : 1.f;
+    dw = fmaf(s1, S1, dw);
+    db = fmaf(s1, S0, db);
+    dwp = fmaf(p.gate >= 0 ? mod_at(p, doc, p.gate, c) : 1.f, S2, dwp);
+    m0 += S0;
+    m1 += w * S1 + b * S0;
+    m2 += wp * S2;
+  }
+  if (out.dw_pre) out.dw_pre[c] = dw;
+  if (out.db_pre) out.db_pre[c] = db;
+  if (out.dw_post) out.dw_post[c] = dwp;
+  if (out.dmod_bias) {
+    if (p.chunk >= 0) {
+      out.dmod_bias[static_cast<int64_t>(3 * p.chunk) * p.D + c] = m0;
+      out.dmod_bias[static_cast<int64_t>(3 * p.chunk + 1) * p.D + c] = m1;
+    }
+    if (p.gate >= 0) out.dmod_bias[static_cast<int64_t>(p.gate) * p.D + c] = m2;
+  }
+}
+
+// Threads of a block: as many units of 8 columns per thread as NU, whole warps.
+int block_threads(int D, int nu) { return (D / 8 + nu * 32 - 1) / (nu * 32) * 32; }
+
+// Blocks of one launch: every resident slot of the card, no more than rows.
+template <typename K>
+int resident_blocks(K kernel, int threads, int rows) {
+  int dev = 0, sms = 0, per_sm = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0);
+  int64_t n = static_cast<int64_t>(sms > 0 ? sms : 148) * (per_sm > 0 ? per_sm : 1);
+  n = n < kMaxBlocks ? n : kMaxBlocks;
+  return static_cast<int>(n < rows ? n : (rows > 0 ? rows : 1));
+}
+
+template <typename T, int NU, int kMaxThreads>
+int launch_fwd(const ResNormParams& p, cudaStream_t s) {
+  const int th = block_threads(p.D, NU);
+  auto kernel = gated_residual_norm_kernel<T, NU, kMaxThreads>;
+  kernel<<<resident_blocks(kernel, th, p.rows), th, 0, s>>>(p);
+  return check_launch();
+}
+template <typename T>
+int run_fwd(const ResNormParams& p, cudaStream_t s) {
+  if (p.D <= 2048) return launch_fwd<T, 1, 256>(p, s);
+  return launch_fwd<T, 2, 512>(p, s);
+}
+
+template <typename T, int NU, int kMaxThreads>
+int launch_bwd(const ResNormParams& p, cudaStream_t s, int* blocks) {
+  const int th = block_threads(p.D, NU);
+  auto kernel = gated_residual_norm_bwd_kernel<T, NU, kMaxThreads>;
+  *blocks = resident_blocks(kernel, th, p.rows);
+  kernel<<<*blocks, th, 0, s>>>(p);
+  return check_launch();
+}
+template <typename T>
+int run_bwd(const ResNormParams& p, const wan_residual_norm_grads& g, float* total, cudaStream_t s) {
+  int blocks = 0, st = WAN_OK;
+  if (p.n_docs > 0)
+    st = p.D <= 2048 ? launch_bwd<T, 1, 256>(p, s, &blocks)
+                     : p.D <= 5120 ? launch_bwd<T, 2, 320>(p, s, &blocks) : launch_bwd<T, 2, 512>(p, s, &blocks);
+  if (st != WAN_OK || !p.part) return st;
+  if (p.n_docs > 0) {
+    const int docs_y = p.n_docs < 1024 ? p.n_docs : 1024;
+    resnorm_doc_sums_kernel<T><<<dim3((p.D + 31) / 32, docs_y), dim3(32, 8), 0, s>>>(p, blocks, total, g.de);
+    count_launches(1);
+    st = check_launch();
+  }
+  if (st != WAN_OK || !(g.dmod_bias || g.dw_pre || g.db_pre || g.dw_post)) return st;
+  resnorm_weight_sums_kernel<T><<<(p.D + 127) / 128, 128, 0, s>>>(p, total, g);
+  count_launches(1);
+  return check_launch();
+}
+
+int check_op(const wan_dit_config* cfg, const wan_residual_norm* op, const float* e, const float* mod_bias,
+             const int32_t* cu, int n_docs, int rows) {
+  WAN_TRY(check_cfg(cfg));
+  WAN_REQUIRE(op, WAN_ERR_NULL);
+  WAN_REQUIRE(op->pre == WAN_NORM_LAYER || op->pre == WAN_NORM_RMS, WAN_ERR_SHAPE);
+  WAN_REQUIRE(op->post >= WAN_NORM_NONE && op->post <= WAN_NORM_RMS, WAN_ERR_SHAPE);
+  WAN_REQUIRE(op->gate >= -1 && op->gate <= 5 && op->chunk >= -1 && op->chunk <= 1, WAN_ERR_SHAPE);
+  // one row of e is either the gate or a shift or scale: its gradient has one place
+  WAN_REQUIRE(op->gate < 0 || op->chunk < 0 || (op->gate != 3 * op->chunk && op->gate != 3 * op->chunk + 1),
+              WAN_ERR_SHAPE);
+  WAN_REQUIRE(op->residual_scale - op->residual_scale == 0.f, WAN_ERR_SHAPE);  // finite
+  WAN_REQUIRE(op->post != WAN_NORM_NONE || !op->w_post, WAN_ERR_SHAPE);
+  WAN_REQUIRE(cfg->dim <= 8192, WAN_ERR_UNSUPPORTED);
+  WAN_REQUIRE(rows >= 0 && n_docs >= 0, WAN_ERR_SHAPE);
+  WAN_TRY(check_opt_ptr(op->w_pre));
+  WAN_TRY(check_opt_ptr(op->b_pre));
+  WAN_TRY(check_opt_ptr(op->w_post));
+  WAN_TRY(check_opt_ptr(mod_bias));
+  if (op->gate >= 0 || op->chunk >= 0) WAN_TRY(check_array(e, n_docs));
+  WAN_TRY(check_ptr(cu));
+  return WAN_OK;
+}
+
+ResNormParams make_params(const wan_dit_config* cfg, const wan_residual_norm* op, const float* x, const void* y,
+                          const float* e, const float* mod_bias, const int32_t* cu, int n_docs, int rows) {
+  ResNormParams p{};
+  p.x = x, p.y = y, p.e = e, p.mod_bias = mod_bias, p.cu = cu;
+  p.n_docs = n_docs, p.rows = rows, p.D = cfg->dim;
+  p.pre = op->pre, p.post = op->post, p.gate = op->gate, p.chunk = op->chunk;
+  p.residual_scale = op->residual_scale, p.eps = cfg->eps;
+  p.w_pre = op->w_pre, p.b_pre = op->b_pre, p.w_post = op->w_post;
+  return p;
+}
+
+}  // namespace
+}  // namespace wan
+
+using namespace wan;
+
+extern "C" {
+
+int wan_gated_residual_norm_fwd(const wan_dit_config* cfg, const wan_residual_norm* op, const float* x, const void* y,
+                                const float* e, const float* mod_bias, const int32_t* cu_rows, int n_docs, int rows,
+                                float* x_out, void* h_out, void* stream) {
+  WAN_TRY(check_op(cfg, op, e, mod_bias, cu_rows, n_docs, rows));
+  WAN_TRY(check_array(x, rows));
+  WAN_TRY(check_array(y, rows));
+  WAN_TRY(check_array(x_out, rows));
+  WAN_TRY(check_array(h_out, rows));
+  if (rows == 0 || n_docs == 0) return WAN_OK;
+  ResNormParams p = make_params(cfg, op, x, y, e, mod_bias, cu_rows, n_docs, rows);
+  p.x_out = x_out, p.h_out = h_out;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  trace_launch_begin(WAN_KIND_NORM, s, static_cast<double>(rows) * cfg->dim * 2.0 * (4 + dtype_size(cfg->dtype)));
+  const int st = cfg->dtype == WAN_BF16 ? run_fwd<__nv_bfloat16>(p, s) : run_fwd<float>(p, s);
+  trace_launch_end(WAN_KIND_NORM, s);
+  return st;
+}
+
+size_t wan_gated_residual_norm_workspace_bytes(const wan_dit_config* cfg, int rows, int n_docs) {
+  if (check_cfg(cfg) != WAN_OK || rows < 0 || n_docs < 0) return 0;
+  const int64_t blocks = rows < kMaxBlocks ? rows : kMaxBlocks;
+  // partial rows of every (block, document) slot, then the documents' sums
+  return static_cast<size_t>(blocks + 2 * static_cast<int64_t>(n_docs)) * 3 * cfg->dim * 4;
+}
+
+int wan_gated_residual_norm_bwd(const wan_dit_config* cfg, const wan_residual_norm* op, const float* x_out,
+                                const void* y, const float* e, const float* mod_bias, const int32_t* cu_rows,
+                                int n_docs, int rows, const void* dh, const float* dx_out, float* dx, void* dy,
+                                const wan_residual_norm_grads* grads, void* workspace, size_t ws_bytes, void* stream) {
+  WAN_TRY(check_op(cfg, op, e, mod_bias, cu_rows, n_docs, rows));
+  WAN_TRY(check_array(x_out, rows));
+  WAN_TRY(check_array(y, rows));
+  WAN_TRY(check_array(dh, rows));
+  WAN_TRY(check_opt_ptr(dx_out));
+  WAN_TRY(check_array(dx, rows));
+  WAN_TRY(check_array(dy, rows));
+  wan_residual_norm_grads g{};
+  if (grads) g = *grads;
+  for (const float* q : {g.de, g.dmod_bias, g.dw_pre, g.db_pre, g.dw_post}) WAN_TRY(check_opt_ptr(q));
+  const bool sums = g.de || g.dmod_bias || g.dw_pre || g.db_pre || g.dw_post;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((n_docs == 0 || rows == 0) && !sums) return WAN_OK;
+  ResNormParams p = make_params(cfg, op, x_out, y, e, mod_bias, cu_rows, n_docs, rows);
+  p.dh = dh, p.dx_out = dx_out, p.dx = dx, p.dy = dy;
+  float* total = nullptr;
+  if (sums) {
+    WAN_TRY(check_ptr(workspace));
+    WAN_REQUIRE(ws_bytes >= wan_gated_residual_norm_workspace_bytes(cfg, rows, n_docs), WAN_ERR_WORKSPACE);
+    p.part = static_cast<float*>(workspace);
+    const int64_t blocks = rows < kMaxBlocks ? rows : kMaxBlocks;
+    total = p.part + (blocks + n_docs) * 3 * static_cast<int64_t>(cfg->dim);
+  }
+  trace_launch_begin(WAN_KIND_NORM, s, static_cast<double>(rows) * cfg->dim * (12 + 3.0 * dtype_size(cfg->dtype)));
+  const int st = cfg->dtype == WAN_BF16 ? run_bwd<__nv_bfloat16>(p, g, total, s) : run_bwd<float>(p, g, total, s);
+  trace_launch_end(WAN_KIND_NORM, s);
+  return st;
+}
+
+}  // extern "C"
