@@ -643,8 +643,8 @@ int wan_attention_packed_bwd(const wan_dit_config* cfg, const wan_documents* doc
                              int kv_heads, const wan_rows* q, const wan_rows* k, const wan_rows* v, const wan_rows* o,
                              const float* lse, const wan_rows* d_o, const wan_rows* dq, const wan_rows* dk,
                              const wan_rows* dv, void* workspace, size_t ws_bytes, void* stream);
-/* Bytes of the forward's (backward = 0) or the gradient's (1) workspace; one buffer of the
- * larger size serves both in turn. 0 on a bad config. */
+/* Bytes of the forward's workspace (backward = 0), or of one that serves the forward and
+ * the gradient in turn (1). 0 on a bad config. */
 size_t wan_attention_packed_workspace_bytes(const wan_dit_config* cfg, int q_rows, int k_rows, int n_docs,
                                             int kv_heads, int backward);
 

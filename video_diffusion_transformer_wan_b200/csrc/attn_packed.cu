@@ -47,8 +47,14 @@ size_t wan_attention_packed_workspace_bytes(const wan_dit_config* cfg, int q_row
   if (check_cfg(cfg, true) != WAN_OK || q_rows < 0 || k_rows < 0 || n_docs < 0 || kv_heads < 1 ||
       cfg->heads % kv_heads != 0)
     return 0;
-  if (backward) return (static_cast<size_t>(cfg->heads) * q_rows * 4 + 255) / 256 * 256;
-  return 0;
+  size_t bytes = 0;
+  if (cfg->dtype == WAN_BF16) {
+    PackedAttn a{};
+    a.H = cfg->heads, a.Hk = kv_heads, a.q_rows = q_rows;
+    bytes = attn_packed_tc_workspace(a);
+  }
+  const size_t grad = (static_cast<size_t>(cfg->heads) * q_rows * 4 + 255) / 256 * 256;
+  return backward && grad > bytes ? grad : bytes;
 }
 
 int wan_attention_packed_fwd(const wan_dit_config* cfg, const wan_documents* docs, int q_rows, int k_rows,
@@ -60,10 +66,10 @@ int wan_attention_packed_fwd(const wan_dit_config* cfg, const wan_documents* doc
   for (const wan_rows* t : {k, v}) WAN_TRY(check_view(t, k_rows, wk, cfg->dtype, true));
   WAN_TRY(check_opt_ptr(lse));
   WAN_TRY(check_opt_ptr(workspace));
-  (void)ws_bytes;
   if (q_rows == 0 || docs->n_docs == 0) return WAN_OK;
   PackedAttn p = make_packed(cfg, docs, q_rows, k_rows, kv_heads, q, k, v, o);
   p.lse = lse;
+  if (cfg->dtype == WAN_BF16) return launch_attn_packed_tc(p, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
   return launch_attn_packed_simt(p, cfg->dtype, static_cast<cudaStream_t>(stream));
 }
 

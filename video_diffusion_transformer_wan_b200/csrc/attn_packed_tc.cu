@@ -1,0 +1,730 @@
+// Attention inside packed documents on the sm_100a tensor cores (bf16, head_dim 128):
+// o = softmax(s) v over each query's seen keys, one pass over the keys with a running
+// maximum and sum, and the log-sum for the gradient.
+//
+// A unit of work is two 128-row query tiles of one document and head group (see
+// packed_tc.cuh) against the document's keys. A CTA's warps share it as follows (384
+// threads, one CTA per SM, looping over its work):
+//   warp 0   : TMA loads: both Q tiles, then K_0, K_1, V_0, K_2, V_1, ... through a
+//              5-stage ring of 32 KB tiles;
+//   warp 1   : tcgen05.mma: for key tile j and query tile t, O_t += P_t(j-1) V_{j-1} with
+//              P from tensor memory, then S_t = Q_t K_j^T;
+//   warp 3   : finds this CTA's share of the work; warp 2 notes where it ends;
+//   warps 4-7, 8-11: softmax of tile 0 and tile 1, a thread per row: the row's 128 scores
+//              come from TMEM at once; cap, distance and mask passes run over them only
+//              where the call, or the tile, has any; P goes back over S in bf16 (the
+//              operand's rounding; sums stay fp32). The base of the exponentials moves only
+//              when the row maximum grew by more than 2^8.
+// While one tile's softmax runs, the tensor core works on the other's products.
+//
+// Work is cut by key tiles: with T key tiles over all units and C CTAs, CTA c takes tiles
+// [T c / C, T (c+1) / C), so that any mix of document lengths, orders of keys and few
+// queries over many keys load the SMs alike. A unit cut between CTAs leaves unnormalised
+// outputs with their base and sum in the workspace, merged in CTA order by a second kernel
+// (nothing depends on timing). Units of up to 8 key tiles, and all units when there is no
+// workspace, stay whole in the CTA in which they begin.
+//
+// Keys behind a document's end are masked by position, and their V rows, which belong to
+// other documents or to none, are cleared in shared memory before the product.
+#include <math.h>
+
+#include <mutex>
+
+#include "internal.h"
+#include "packed_tc.cuh"
+
+namespace wan {
+namespace {
+
+constexpr int kRegsLow = 88;    // warps 0-3
+constexpr int kRegsHigh = 208;  // softmax warps: a whole score row in registers
+static_assert(128 * kRegsLow + 256 * kRegsHigh <= 384 * 168, "register split above the launch");
+constexpr int kThreads = 384;
+constexpr int kStages = 5;
+constexpr int kMaxCtas = 148;
+constexpr int kMinSplit = 8;         // a unit of more key tiles may be cut
+constexpr int kMinShare = 4;         // key tiles a CTA takes at least
+constexpr float kRescaleLog2 = 8.0f;
+constexpr size_t kSmem = 1024 + static_cast<size_t>(kPkTileBytes) * (2 + kStages) + 512;
+
+// Where a CTA's share ends inside a unit that begins in it: what the merge needs.
+struct Cut {
+  int crosses, first_slot, last_cta, row0, rows, group;
+};
+
+struct FwdParams {
+  PackedAttn a;
+  int pack, per_tile, groups;   // heads per tile, queries per tile, head groups
+  int ctas, may_split, slot_rows;
+  float mult;                   // log2 units per (possibly capped) score
+  float cap_in;                 // scale / cap (cap > 0)
+  int prescale;                 // slopes, or a negative scale: scores are scaled before the maximum
+  float* part_o;                // [2 ctas][slot_rows][128]
+  float2* part_ml;              // [2 ctas][slot_rows]: base (log2 units), sum
+  Cut* cuts;                    // [ctas]
+  int* err;
+};
+
+// ------------------------------------------------------------------ the share of a CTA
+__device__ __forceinline__ int tiles_seen(const DocRows& d, const FwdParams& p, int first, int count) {
+  const int last = min(first + count, d.Lq) - 1;  // rows see ever more keys
+  return div_up(seen_keys(last, d.off, d.Lk, d.prefix, p.a.causal_block), kPkTile);
+}
+// Key tiles of unit `u` (pair of query tiles) of a document; a unit that sees none counts
+// as one, it still writes its rows.
+__device__ __forceinline__ int unit_tiles(const DocRows& d, const FwdParams& p, int u) {
+  return max(1, tiles_seen(d, p, u * 2 * p.per_tile, 2 * p.per_tile));
+}
+
+template <typename T>
+__device__ __forceinline__ T warp_incl_scan(T v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T up = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += up;
+  }
+  return v;
+}
+
+// Key tiles of the lane's document d over all its units (whole warp; d >= n_docs: 0).
+__device__ int64_t doc_tiles(const FwdParams& p, int d) {
+  int64_t w = 0;
+  int units = 0;
+  bool walk = false;
+  DocRows doc{};
+  if (d < p.a.n_docs) {
+    doc = load_doc(p.a, d);
+    units = div_up(doc.Lq, 2 * p.per_tile);
+    if (units > 0 && p.a.causal_block == 0) {
+      w = static_cast<int64_t>(units) * unit_tiles(doc, p, 0);
+    } else if (units <= 8) {
+      for (int u = 0; u < units; ++u) w += unit_tiles(doc, p, u);
+    } else {
+      walk = true;
+    }
+  }
+  for (unsigned todo = __ballot_sync(0xffffffffu, walk); todo; todo &= todo - 1) {
+    const int src = __ffs(todo) - 1;
+    const DocRows x = load_doc(p.a, d - static_cast<int>(threadIdx.x & 31) + src);
+    const int n = div_up(x.Lq, 2 * p.per_tile);
+    int64_t s = 0;
+    for (int u = threadIdx.x & 31; u < n; u += 32) s += unit_tiles(x, p, u);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (static_cast<int>(threadIdx.x & 31) == src) w = s;
+  }
+  return w;
+}
+
+struct Share {
+  int64_t s, e;   // this CTA's key tiles
+  int64_t total;  // all key tiles
+  int64_t at;     // first key tile of the unit below
+  int ctas;       // CTAs that have work
+  int group, doc, unit;
+};
+
+__device__ void find_share(const FwdParams& p, Share& out) {
+  const int lane = threadIdx.x & 31;
+  int64_t per_group = 0;
+  for (int d0 = 0; d0 < p.a.n_docs; d0 += 32) per_group += __shfl_sync(0xffffffffu, warp_incl_scan(doc_tiles(p, d0 + lane)), 31);
+  Share sh{};
+  sh.total = per_group * p.groups;
+  const int64_t most = sh.total / kMinShare;
+  sh.ctas = most < 1 ? 1 : (most < p.ctas ? static_cast<int>(most) : p.ctas);
+  const int c = blockIdx.x;
+  sh.s = c < sh.ctas ? sh.total * c / sh.ctas : sh.total;
+  sh.e = c < sh.ctas ? sh.total * (c + 1) / sh.ctas : sh.total;
+  if (sh.s < sh.e) {
+    sh.group = static_cast<int>(sh.s / per_group);
+    int64_t left = sh.s - per_group * sh.group;
+    sh.at = sh.s - left;
+    for (int d0 = 0;; d0 += 32) {
+      const int64_t w = doc_tiles(p, d0 + lane), incl = warp_incl_scan(w), sum = __shfl_sync(0xffffffffu, incl, 31);
+      if (left >= sum) {
+        left -= sum, sh.at += sum;
+        continue;
+      }
+      const int src = __ffs(__ballot_sync(0xffffffffu, left < incl)) - 1;
+      const int64_t before = __shfl_sync(0xffffffffu, incl - w, src);
+      sh.doc = d0 + src;
+      left -= before, sh.at += before;
+      break;
+    }
+    const DocRows doc = load_doc(p.a, sh.doc);
+    const int units = div_up(doc.Lq, 2 * p.per_tile);
+    if (p.a.causal_block == 0) {
+      const int n = unit_tiles(doc, p, 0);
+      sh.unit = static_cast<int>(left / n);
+      sh.at += static_cast<int64_t>(sh.unit) * n;
+    } else {
+      for (int u0 = 0;; u0 += 32) {
+        const int64_t w = u0 + lane < units ? unit_tiles(doc, p, u0 + lane) : 0, incl = warp_incl_scan(w);
+        const int64_t sum = __shfl_sync(0xffffffffu, incl, 31);
+        if (left >= sum) {
+          left -= sum, sh.at += sum;
+          continue;
+        }
+        const int src = __ffs(__ballot_sync(0xffffffffu, left < incl)) - 1;
+        sh.unit = u0 + src;
+        sh.at += __shfl_sync(0xffffffffu, incl - w, src);
+        break;
+      }
+    }
+  }
+  if (lane == 0) out = sh;
+}
+
+// One piece of a CTA's work: key tiles [k0, k0 + nmax) of a unit.
+struct Piece {
+  DocRows d;
+  int group, first;     // head group, first query row of the unit
+  int k0, n[2], nmax;   // key tiles of each query tile from key tile k0 on
+  bool whole, begins;   // the unit is not cut; the piece holds its beginning
+  int slot;             // partial results of a cut unit
+  int end;              // the unit's end, relative to the share
+};
+
+// Walks the pieces of a CTA in order. Positions are relative to the share's first key tile
+// and the step to the next unit is taken on the next call: little state stays live between.
+class Walker {
+ public:
+  __device__ Walker(const FwdParams& p, const Share& s)
+      : p_(p), at_(static_cast<int>(s.at - s.s)), end_(static_cast<int>(s.e - s.s)), n_(0), group_(s.group), doc_(s.doc),
+        unit_(s.unit - 1) {
+    if (end_ > 0) d_ = load_doc(p.a, doc_);
+  }
+  __device__ bool next(Piece& x) {
+    while (at_ + n_ < end_) {
+      at_ += n_;
+      ++unit_;
+      while (unit_ * 2 * static_cast<int64_t>(p_.per_tile) >= d_.Lq) {
+        unit_ = 0;
+        if (++doc_ >= p_.a.n_docs) doc_ = 0, ++group_;
+        d_ = load_doc(p_.a, doc_);
+      }
+      n_ = unit_tiles(d_, p_, unit_);
+      const bool may_cut = p_.may_split && n_ > kMinSplit;
+      int a = 0, b = n_;
+      bool mine = at_ >= 0;
+      if (may_cut) {
+        a = max(0, -at_);
+        b = min(n_, end_ - at_);
+        mine = a < b;
+      }
+      if (!mine) continue;
+      x.d = d_, x.group = group_, x.first = unit_ * 2 * p_.per_tile;
+      x.k0 = a;
+      x.nmax = 0;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int f = x.first + t * p_.per_tile;
+        x.n[t] = f < d_.Lq ? max(0, min(tiles_seen(d_, p_, f, p_.per_tile), b) - a) : 0;
+        x.nmax = max(x.nmax, x.n[t]);
+      }
+      x.whole = a == 0 && b == n_;
+      x.begins = a == 0;
+      x.slot = 2 * static_cast<int>(blockIdx.x) + (at_ <= 0 ? 0 : 1);  // the CTA's first piece, or its last
+      x.end = at_ + n_;
+      return true;
+    }
+    return false;
+  }
+
+ private:
+  const FwdParams& p_;
+  int at_, end_, n_;  // unit's first key tile, the share's end, the unit's key tiles (0: none yet)
+  int group_, doc_, unit_;
+  DocRows d_{};
+};
+
+// Ring position of K_j / V_j in the load order K_0, K_1, V_0, K_2, V_1, ..., V_{n-1}.
+__device__ __forceinline__ int pos_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
+__device__ __forceinline__ int pos_v(int j, int n) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; }
+
+__global__ void __launch_bounds__(kThreads, 1)
+    packed_fwd_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
+                         const __grid_constant__ CUtensorMap mapV, const __grid_constant__ FwdParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;                        // [2][tile]
+  uint8_t* sKV = sQ + 2 * kPkTileBytes;      // [kStages][tile]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + kStages * kPkTileBytes);
+  uint64_t* q_full = bars;
+  uint64_t* q_empty = bars + 1;
+  uint64_t* kv_full = bars + 2;
+  uint64_t* kv_empty = kv_full + kStages;
+  uint64_t* s_full = kv_empty + kStages;     // [2]
+  uint64_t* p_full = s_full + 2;             // [2]
+  uint64_t* o_final = p_full + 2;            // [2]
+  uint64_t* drain = o_final + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  Share* share = reinterpret_cast<Share*>(drain + 2);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_full[t], 128);
+      mbar_init(&o_final[t], 1);
+    }
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&mapQ);
+    tma_prefetch_desc(&mapK);
+    tma_prefetch_desc(&mapV);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  if (warp == 3) find_share(p, *share);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  Walker walk(p, *share);
+  Piece x;
+
+  if (warp < 4) {
+    setmaxnreg_dec<kRegsLow>();
+    if (warp == 0) {
+      if (lane == 0) {
+        int issued = 0, q_loads = 0;
+        bool ok = true;
+        const uint32_t q_bytes = static_cast<uint32_t>(p.per_tile * p.pack) * 256u;
+        while (ok && walk.next(x)) {
+          if (x.nmax == 0) continue;
+          if (q_loads > 0 && !mbar_wait(q_empty, static_cast<uint32_t>((q_loads - 1) & 1), p.err)) break;
+          mbar_arrive_expect_tx(q_full, q_bytes * ((x.n[0] > 0) + (x.n[1] > 0)));
+          for (int t = 0; t < 2; ++t)
+            if (x.n[t] > 0)
+              for (int c = 0; c < 2; ++c)
+                tma_load_3d(sQ + t * kPkTileBytes + c * kPkSpan, &mapQ, q_full, 64 * c, x.group * p.pack,
+                            x.d.q0 + x.first + t * p.per_tile);
+          ++q_loads;
+          const int col = x.group * p.pack / (p.a.H / p.a.Hk) * kPkD;
+          const int n_loads = 2 * x.nmax;
+          for (int ld = 0; ld < n_loads; ++ld) {
+            const int stage = issued % kStages;
+            if (!mbar_wait(&kv_empty[stage], static_cast<uint32_t>((issued / kStages) & 1) ^ 1u, p.err)) {
+              ok = false;
+              break;
+            }
+            const bool is_v = ld == n_loads - 1 || (ld > 0 && !(ld & 1));
+            const int j = is_v ? (ld == n_loads - 1 ? x.nmax - 1 : (ld >> 1) - 1) : (ld + 1) >> 1;
+            mbar_arrive_expect_tx(&kv_full[stage], kPkTileBytes);
+            for (int c = 0; c < 2; ++c)
+              tma_load_2d(sKV + stage * kPkTileBytes + c * kPkSpan, is_v ? &mapV : &mapK, &kv_full[stage], col + 64 * c,
+                          x.d.k0 + (x.k0 + j) * kPkTile);
+            ++issued;
+          }
+        }
+        // Wait for every copy this thread started (the last fill of each buffer and stage).
+        if (q_loads > 0) mbar_wait(q_full, static_cast<uint32_t>((q_loads - 1) & 1), p.err);
+        for (int s = 0; s < kStages; ++s) {
+          const int n_s = issued / kStages + (s < issued % kStages ? 1 : 0);
+          if (n_s > 0) mbar_wait(&kv_full[s], static_cast<uint32_t>((n_s - 1) & 1), p.err);
+        }
+      }
+    } else if (warp == 1) {
+      // The whole warp walks and waits (it clears ragged V rows together); lane 0 issues.
+      const uint32_t idesc_qk = idesc_bf16_f32(kPkTile, kPkTile, 0, 0), idesc_pv = idesc_bf16_f32(kPkTile, kPkD, 0, 1);
+      const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t k_desc = sdesc_sw128(smem_u32(sKV), 16, 1024);
+      const uint64_t v_desc = sdesc_sw128(smem_u32(sKV), kPkSpan, 1024);
+      auto wait_pos = [&](int pos) {
+        return mbar_wait_warp(&kv_full[pos % kStages], static_cast<uint32_t>((pos / kStages) & 1), p.err);
+      };
+      auto pv = [&](int t, bool first, int stage) {
+        if (lane == 0) {
+          const uint64_t vd = v_desc + static_cast<uint32_t>((stage * kPkTileBytes) >> 4);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            tc_mma_bf16_ts(tmem_base + 256 + t * kPkTile, tmem_base + t * kPkTile + k * 8, vd + ((k * 16 * 128) >> 4),
+                           idesc_pv, (!first || k > 0) ? 1u : 0u);
+        }
+      };
+      auto qk = [&](int t, int stage) {
+        if (lane == 0) {
+          const uint64_t qd = q_desc + static_cast<uint32_t>((t * kPkTileBytes) >> 4);
+          const uint64_t kd = k_desc + static_cast<uint32_t>((stage * kPkTileBytes) >> 4);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t off = ((k >> 2) * kPkSpan + (k & 3) * 32) >> 4;
+            tc_mma_bf16(tmem_base + t * kPkTile, qd + off, kd + off, idesc_qk, k > 0 ? 1u : 0u);
+          }
+          tc_commit(&s_full[t]);
+        }
+      };
+      int base = 0, units = 0;
+      uint32_t p_seen[2] = {0, 0};  // key tiles whose P was waited for
+      bool ok = true;
+      while (ok && walk.next(x)) {
+        if (x.nmax == 0) continue;
+        if (!mbar_wait_warp(q_full, static_cast<uint32_t>(units & 1), p.err)) break;
+        ++units;
+        for (int j = 0; ok && j < x.nmax; ++j) {
+          const int pk = base + pos_k(j), pvp = base + pos_v(j - 1, x.nmax);
+          if (!wait_pos(pk) || (j > 0 && !wait_pos(pvp))) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (j > 0 && j - 1 < x.n[t]) {
+              if (!mbar_wait_warp(&p_full[t], p_seen[t] & 1u, p.err)) {
+                ok = false;
+                break;
+              }
+              ++p_seen[t];
+              // The first product of a piece overwrites O_t: the softmax threads read the
+              // piece before out of it before they arrived here for this one.
+              tc_fence_after();
+              pv(t, j == 1, pvp % kStages);
+              if (j == x.n[t] && lane == 0) tc_commit(&o_final[t]);  // tile t ends before the other
+            }
+            if (j < x.n[t]) qk(t, pk % kStages);
+          }
+          if (!ok) break;
+          if (lane == 0) {
+            tc_commit(&kv_empty[pk % kStages]);
+            if (j > 0) tc_commit(&kv_empty[pvp % kStages]);
+          }
+        }
+        if (!ok) break;
+        if (lane == 0) tc_commit(q_empty);
+        const int pvp = base + pos_v(x.nmax - 1, x.nmax);
+        if (!wait_pos(pvp)) break;
+        const int end = x.d.Lk - (x.k0 + x.nmax - 1) * kPkTile;  // keys of the last tile that are the document's
+        if (end < kPkTile) zero_tile_rows(sKV + (pvp % kStages) * kPkTileBytes, end);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (x.n[t] != x.nmax) continue;
+          if (!mbar_wait_warp(&p_full[t], p_seen[t] & 1u, p.err)) {
+            ok = false;
+            break;
+          }
+          ++p_seen[t];
+          tc_fence_after();
+          pv(t, x.nmax == 1, pvp % kStages);
+          if (lane == 0) tc_commit(&o_final[t]);
+        }
+        if (!ok) break;
+        if (lane == 0) tc_commit(&kv_empty[pvp % kStages]);
+        base += 2 * x.nmax;
+      }
+      if (lane == 0) {
+        tc_commit(drain);
+        mbar_wait(drain, 0, p.err);
+      }
+      __syncwarp();
+    } else if (warp == 2 && p.may_split) {
+      Cut cut{};
+      while (walk.next(x)) {
+        if (x.whole || !x.begins) continue;
+        cut.crosses = 1;
+        cut.first_slot = x.slot;
+        // CTA of the unit's last key tile
+        cut.last_cta = static_cast<int>(((share->s + x.end) * share->ctas - 1) / share->total);
+        cut.row0 = x.d.q0 + x.first;
+        cut.rows = min(2 * p.per_tile, x.d.Lq - x.first);
+        cut.group = x.group;
+      }
+      if (lane == 0) p.cuts[blockIdx.x] = cut;
+    }
+  } else {
+    setmaxnreg_inc<kRegsHigh>();
+    const int t = (warp - 4) >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_row = tmem_base + lane_off + t * kPkTile;
+    const uint32_t o_row = tmem_base + lane_off + 256 + t * kPkTile;
+    const int query = row / p.pack, head_in = row - query * p.pack;
+    uint32_t s_seen = 0, o_seen = 0;
+    bool ok = true;
+    while (ok && walk.next(x)) {
+      const int i = x.first + t * p.per_tile + query;
+      const bool live = query < p.per_tile && i < x.d.Lq;
+      const int head = x.group * p.pack + head_in;
+      // Rows of no query are not masked: what they hold goes nowhere.
+      const int seen = live ? seen_keys(i, x.d.off, x.d.Lk, x.d.prefix, p.a.causal_block) : 0x7fffffff;
+      const float slope2 = p.a.slopes && live ? __ldg(p.a.slopes + head) * kLog2e : 0.f;
+      const float mult = p.prescale ? 1.0f : p.mult;
+      float m_run = -INFINITY, l_run = 0.f;
+      const int n = t == 0 ? x.n[0] : x.n[1];
+      for (int j = 0; j < n; ++j) {
+        if (!mbar_wait_warp(&s_full[t], s_seen & 1u, p.err)) {
+          ok = false;
+          break;
+        }
+        ++s_seen;
+        tc_fence_after();
+        uint32_t r[kPkTile];
+        tmem_ld32(s_row, *reinterpret_cast<uint32_t(*)[32]>(r));
+        tmem_ld32(s_row + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
+        tmem_ld32(s_row + 64, *reinterpret_cast<uint32_t(*)[32]>(r + 64));
+        tmem_ld32(s_row + 96, *reinterpret_cast<uint32_t(*)[32]>(r + 96));
+        tmem_ld_wait();
+        const int key0 = (x.k0 + j) * kPkTile;
+        if (p.a.cap > 0.f) cap_scores(r, p.cap_in, live);
+        if (p.prescale) {
+          const float from = static_cast<float>(i + x.d.off - key0);
+#pragma unroll
+          for (int c = 0; c < kPkTile; ++c)
+            r[c] = __float_as_uint(fmaf(__uint_as_float(r[c]), p.mult, -slope2 * fabsf(from - static_cast<float>(c))));
+        }
+        const int valid = seen - key0;
+        if (valid < kPkTile) {
+#pragma unroll
+          for (int c = 0; c < kPkTile; ++c)
+            if (c >= valid) r[c] = __float_as_uint(-INFINITY);
+        }
+        float mx8[8];
+#pragma unroll
+        for (int a = 0; a < 8; ++a) mx8[a] = __uint_as_float(r[a]);
+#pragma unroll
+        for (int c = 8; c < kPkTile; c += 2)
+          mx8[(c >> 1) & 7] = fmax3(mx8[(c >> 1) & 7], __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
+        const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
+                               fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+        const bool grow = live && (mx - m_run) * mult > kRescaleLog2;
+        float alpha = 1.0f;
+        bool rescale = false;
+        if (j == 0) {
+          m_run = mx;
+        } else if (__any_sync(0xffffffffu, grow)) {
+          const float m_new = fmaxf(m_run, mx);
+          alpha = m_new == -INFINITY ? 1.0f : ex2_approx((m_run - m_new) * mult);
+          m_run = m_new;
+          rescale = true;
+        }
+        const float nb = m_run == -INFINITY ? 0.f : -m_run * mult;  // a row that has seen nothing yet
+        const unsigned long long mult2 = f2_pack(mult, mult), nb2 = f2_pack(nb, nb);
+        unsigned long long rs4[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+        for (int c = 0; c < kPkTile / 2; ++c) {
+          const float2 y = f2_unpack(f2_fma(f2_pack(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])), mult2, nb2));
+          const float e0 = ex2_approx(y.x), e1 = ex2_approx(y.y);
+          rs4[c & 3] = f2_add(rs4[c & 3], f2_pack(e0, e1));
+          r[c] = pack_bf16x2(e0, e1);
+        }
+        tmem_st32(s_row, *reinterpret_cast<uint32_t(*)[32]>(r));
+        tmem_st32(s_row + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
+        if (rescale) {
+          // S_t(j) ready implies that PV_t(j-1) completed, and PV_t(j) waits for this
+          // thread's arrival below: O_t is current and idle here.
+#pragma unroll 1
+          for (int c = 0; c < kPkD / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(o_row + c * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
+            tmem_st32(o_row + c * 32, o);
+          }
+          l_run *= alpha;
+        }
+        {
+          const float2 s01 = f2_unpack(f2_add(rs4[0], rs4[1])), s23 = f2_unpack(f2_add(rs4[2], rs4[3]));
+          l_run += (s01.x + s01.y) + (s23.x + s23.y);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&p_full[t]);
+      }
+      if (!ok) break;
+      if (n > 0) {
+        if (!mbar_wait_warp(&o_final[t], o_seen & 1u, p.err)) break;
+        ++o_seen;
+        tc_fence_after();
+      }
+      const int64_t grow_row = static_cast<int64_t>(x.d.q0) + i;
+      const float base2 = m_run * mult;  // log2 units
+      if (!x.whole) {
+        const int64_t slot = static_cast<int64_t>(x.slot) * p.slot_rows + t * kPkTile + row;
+        float4* po = reinterpret_cast<float4*>(p.part_o + slot * kPkD);
+        if (n > 0) {
+#pragma unroll 1
+          for (int c = 0; c < kPkD / 32; ++c) {
+            uint32_t r0[32];
+            tmem_ld32(o_row + c * 32, r0);
+            tmem_ld_wait();
+            if (live) {
+#pragma unroll
+              for (int g = 0; g < 8; ++g)
+                po[c * 8 + g] = make_float4(__uint_as_float(r0[4 * g]), __uint_as_float(r0[4 * g + 1]),
+                                            __uint_as_float(r0[4 * g + 2]), __uint_as_float(r0[4 * g + 3]));
+            }
+          }
+        }
+        if (live) p.part_ml[slot] = make_float2(base2, l_run);
+      } else {
+        const float inv = l_run == 0.f ? 0.f : 1.0f / l_run;
+        __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.a.o) + grow_row * p.a.o_stride + head * kPkD;
+#pragma unroll 1
+        for (int c = 0; c < kPkD / 32; ++c) {
+          uint32_t r0[32];
+          if (n > 0) {
+            tmem_ld32(o_row + c * 32, r0);
+            tmem_ld_wait();
+          }
+          if (live) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              uint4 v;  // a row without a seen key: 0, whatever O holds
+              v.x = l_run == 0.f ? 0u : pack_bf16x2(__uint_as_float(r0[8 * g]) * inv, __uint_as_float(r0[8 * g + 1]) * inv);
+              v.y = l_run == 0.f ? 0u : pack_bf16x2(__uint_as_float(r0[8 * g + 2]) * inv, __uint_as_float(r0[8 * g + 3]) * inv);
+              v.z = l_run == 0.f ? 0u : pack_bf16x2(__uint_as_float(r0[8 * g + 4]) * inv, __uint_as_float(r0[8 * g + 5]) * inv);
+              v.w = l_run == 0.f ? 0u : pack_bf16x2(__uint_as_float(r0[8 * g + 6]) * inv, __uint_as_float(r0[8 * g + 7]) * inv);
+              reinterpret_cast<uint4*>(orow + c * 32)[g] = v;
+            }
+          }
+        }
+        if (live && p.a.lse)
+          p.a.lse[static_cast<int64_t>(head) * p.a.q_rows + grow_row] =
+              l_run == 0.f ? -INFINITY : (base2 + log2f(l_run)) * 0.6931471805599453f;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
+}
+
+// Merge the parts of the unit that begins in CTA blockIdx.x and ends in a later one: with
+// base b = max b_c and w_c = 2^(b_c - b), o = sum w_c o_c / sum w_c l_c, in CTA order. A
+// warp takes a row, a lane 4 of its 128 columns.
+__global__ void __launch_bounds__(256) packed_merge_kernel(const __grid_constant__ FwdParams p) {
+  const Cut cut = p.cuts[blockIdx.x];
+  if (!cut.crosses) return;
+  const int lane = threadIdx.x & 31, step = gridDim.y * 8;
+  const int c0 = blockIdx.x;
+  for (int m = blockIdx.y * 8 + (threadIdx.x >> 5); m < cut.rows * p.pack; m += step) {
+    const int query = m / p.pack, head = cut.group * p.pack + m - query * p.pack;
+    const int t = query >= p.per_tile ? 1 : 0;
+    const int in_slot = t * kPkTile + m - t * p.per_tile * p.pack;
+    auto slot_of = [&](int c) { return static_cast<int64_t>(c == c0 ? cut.first_slot : 2 * c) * p.slot_rows + in_slot; };
+    float base = -INFINITY;
+    for (int c = c0; c <= cut.last_cta; ++c) {
+      const float2 ml = p.part_ml[slot_of(c)];
+      if (ml.y != 0.f) base = fmaxf(base, ml.x);
+    }
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = c0; c <= cut.last_cta; ++c) {
+      const int64_t slot = slot_of(c);
+      const float2 ml = p.part_ml[slot];
+      if (ml.y == 0.f) continue;
+      const float w = exp2f(ml.x - base);
+      const float4 v = reinterpret_cast<const float4*>(p.part_o + slot * kPkD)[lane];
+      l = fmaf(w, ml.y, l);
+      o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+    }
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    const int64_t row = static_cast<int64_t>(cut.row0) + query;
+    __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.a.o) + row * p.a.o_stride + head * kPkD;
+    reinterpret_cast<uint2*>(orow)[lane] = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (lane == 0 && p.a.lse)
+      p.a.lse[static_cast<int64_t>(head) * p.a.q_rows + row] = l == 0.f ? -INFINITY : (base + log2f(l)) * 0.6931471805599453f;
+  }
+}
+
+struct SplitLayout {
+  int slot_rows;
+  size_t o_bytes, ml_bytes, total;
+};
+SplitLayout split_layout(const PackedAttn& a) {
+  const int pack = packed_heads_per_tile(a.H, a.Hk), per_tile = kPkTile / pack;
+  SplitLayout l{};
+  l.slot_rows = a.q_rows <= per_tile ? a.q_rows * pack : 2 * kPkTile;
+  l.o_bytes = static_cast<size_t>(2 * kMaxCtas) * l.slot_rows * kPkD * 4;
+  l.ml_bytes = (static_cast<size_t>(2 * kMaxCtas) * l.slot_rows * 8 + 15) / 16 * 16;
+  l.total = l.o_bytes + l.ml_bytes + kMaxCtas * sizeof(Cut);
+  return l;
+}
+
+}  // namespace
+
+int packed_heads_per_tile(int H, int Hk) {
+  const int group = H / Hk;
+  for (int n = group < kPkTile ? group : kPkTile; n > 1; --n)
+    if (group % n == 0) return n;
+  return 1;
+}
+
+bool make_packed_q_map(CUtensorMap* map, const void* ptr, int64_t stride, int rows, int H, int pack) {
+  const uint64_t dims[3] = {kPkD, static_cast<uint64_t>(H), static_cast<uint64_t>(rows)};
+  const uint64_t strides[2] = {kPkD * 2, static_cast<uint64_t>(stride) * 2};
+  const uint32_t box[3] = {64, static_cast<uint32_t>(pack), static_cast<uint32_t>(kPkTile / pack)};
+  return make_tmap_bf16(map, ptr, 3, dims, strides, box);
+}
+
+bool make_packed_kv_map(CUtensorMap* map, const void* ptr, int64_t stride, int rows, int Hk) {
+  const uint64_t dims[2] = {static_cast<uint64_t>(Hk) * kPkD, static_cast<uint64_t>(rows)};
+  const uint64_t strides[1] = {static_cast<uint64_t>(stride) * 2};
+  const uint32_t box[2] = {64, kPkTile};
+  return make_tmap_bf16(map, ptr, 2, dims, strides, box);
+}
+
+size_t attn_packed_tc_workspace(const PackedAttn& a) { return split_layout(a).total; }
+
+int launch_attn_packed_tc(const PackedAttn& a, void* ws, size_t ws_bytes, cudaStream_t s) {
+  FwdParams p{};
+  p.a = a;
+  p.pack = packed_heads_per_tile(a.H, a.Hk);
+  p.per_tile = kPkTile / p.pack;
+  p.groups = a.H / p.pack;
+  p.mult = (a.cap > 0.f ? a.cap : a.scale) * kLog2e;
+  p.cap_in = a.cap > 0.f ? a.scale / a.cap : 0.f;
+  p.prescale = a.slopes || p.mult < 0.f;
+  p.err = device_error_flag();
+  int dev = 0, sms = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  p.ctas = sms > 0 && sms < kMaxCtas ? sms : kMaxCtas;
+  const SplitLayout l = split_layout(a);
+  p.slot_rows = l.slot_rows;
+  if (ws) {
+    if (ws_bytes < l.total) return WAN_ERR_WORKSPACE;
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    p.part_o = reinterpret_cast<float*>(w);
+    p.part_ml = reinterpret_cast<float2*>(w + l.o_bytes);
+    p.cuts = reinterpret_cast<Cut*>(w + l.o_bytes + l.ml_bytes);
+    p.may_split = 1;
+  }
+  CUtensorMap mq, mk, mv;
+  // without keys no key is loaded: any valid map will do
+  const bool keys = a.k_rows > 0;
+  if (!make_packed_q_map(&mq, a.q, a.q_stride, a.q_rows, a.H, p.pack) ||
+      !make_packed_kv_map(&mk, keys ? a.k : a.q, keys ? a.k_stride : a.q_stride, keys ? a.k_rows : 1, a.Hk) ||
+      !make_packed_kv_map(&mv, keys ? a.v : a.q, keys ? a.v_stride : a.q_stride, keys ? a.k_rows : 1, a.Hk))
+    return WAN_ERR_CUDA;
+  static std::once_flag once[64];
+  std::call_once(once[dev & 63], [] {
+    cudaFuncSetAttribute(packed_fwd_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+  });
+  trace_launch_begin(WAN_KIND_ATTN, s);
+  packed_fwd_tc_kernel<<<p.ctas, kThreads, kSmem, s>>>(mq, mk, mv, p);
+  int st = check_launch();
+  if (st == WAN_OK && p.may_split) {
+    packed_merge_kernel<<<dim3(p.ctas, 4), 256, 0, s>>>(p);
+    count_launches(1);
+    st = check_launch();
+  }
+  trace_launch_end(WAN_KIND_ATTN, s);
+  return st;
+}
+
+}  // namespace wan

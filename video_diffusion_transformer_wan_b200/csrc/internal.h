@@ -174,6 +174,15 @@ struct PackedAttn {
   int64_t do_stride, dq_stride, dk_stride, dv_stride;
   float* delta;           // gradient: [H, q_rows], row sums of do * o
 };
+// bf16, head_dim 128, on the tensor cores. ws (NULL: work is not split over the keys) of at
+// least attn_packed_tc_workspace bytes, which depend on q_rows and the head counts.
+int launch_attn_packed_tc(const PackedAttn& p, void* ws, size_t ws_bytes, cudaStream_t s);
+size_t attn_packed_tc_workspace(const PackedAttn& p);
+// Heads of one key head that share a tile of packed query rows, and tensor maps of such
+// tiles ([128 rows / pack queries][pack heads][64 dims]) and of key tiles.
+int packed_heads_per_tile(int H, int Hk);
+bool make_packed_q_map(CUtensorMap* map, const void* ptr, int64_t stride, int rows, int H, int pack);
+bool make_packed_kv_map(CUtensorMap* map, const void* ptr, int64_t stride, int rows, int Hk);
 // CUDA cores, fp32 arithmetic, head_dim <= 128 (act = dtype).
 int launch_attn_packed_simt(const PackedAttn& p, int dtype, cudaStream_t s);
 int launch_attn_packed_simt_bwd(const PackedAttn& p, int dtype, cudaStream_t s);

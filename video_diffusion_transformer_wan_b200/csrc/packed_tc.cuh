@@ -1,0 +1,88 @@
+// Device helpers shared by the tensor-core kernels of the attention inside packed
+// documents: tiles of packed rows, the capped score, and ragged tiles.
+#pragma once
+#include "internal.h"
+#include "packed.cuh"
+#include "ptx.cuh"
+
+namespace wan {
+
+constexpr int kPkTile = 128;                 // packed query rows per tile = keys per tile
+constexpr int kPkD = 128;                    // head dim
+constexpr int kPkSpan = kPkTile * 128;       // 128 rows of one 128-byte swizzled span
+constexpr int kPkTileBytes = 2 * kPkSpan;    // a bf16 tile: two 64-column spans
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Query heads that share a key head lie next to one another, so a tile of 128 rows takes
+// `pack` heads of 128 / pack queries: row m is query m / pack, head m % pack of the tile.
+// pack is the largest divisor of heads / kv_heads up to 128; the key head is then read once
+// for all of them, which is what bounds a step of single tokens over long keys. (A "head
+// group" below is such a set of `pack` heads.)
+struct DocRows {
+  int q0, Lq, k0, Lk, off, prefix;
+};
+__device__ __forceinline__ DocRows load_doc(const PackedAttn& p, int d) {
+  const DocRange a = doc_range(p.cu_q, d, p.q_rows), b = doc_range(p.cu_k, d, p.k_rows);
+  return {a.first, a.count, b.first, b.count, b.count - a.count, p.prefix ? __ldg(p.prefix + d) : 0};
+}
+
+__device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
+
+// Zero rows [row0, 128) of a bf16 tile in shared memory, by one warp: rows behind a
+// document's end may hold anything (NaN too), and 0 * NaN would reach the sums. Whole rows
+// are cleared, so the swizzle inside a row does not matter. Ordered before later reads of
+// the tile by tensor-core instructions of this warp.
+__device__ __forceinline__ void zero_tile_rows(uint8_t* tile, int row0) {
+  const int lane = threadIdx.x & 31;
+  for (int i = row0 * 8 + lane; i < kPkTile * 8; i += 32) {
+    *reinterpret_cast<uint4*>(tile + i * 16) = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(tile + kPkSpan + i * 16) = make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// tanh on the FMA pipes for |y| <= 1/2: an odd polynomial fitted for least largest error of
+// tanh(y)/y on that range (1.3e-8; 2^-24 absolute with its fp32 roundings).
+constexpr float kTanhPolyLimit = 0.5f;
+__device__ __forceinline__ unsigned long long f2_mul(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long f2_splat(float v) { return f2_pack(v, v); }
+__device__ __forceinline__ unsigned long long tanh_poly2(unsigned long long y) {
+  const unsigned long long z = f2_mul(y, y);
+  unsigned long long p = f2_fma(f2_splat(0.017151299864053726f), z, f2_splat(-0.05299423262476921f));
+  p = f2_fma(p, z, f2_splat(0.13324907422065735f));
+  p = f2_fma(p, z, f2_splat(-0.33333075046539307f));
+  p = f2_fma(p, z, f2_splat(1.0f));
+  return f2_mul(p, y);
+}
+// Any y, 2^-22 absolute: 1 - 2 / (e^(2|y|) + 1) with y's sign.
+__device__ __forceinline__ float tanh_exp(float y) {
+  const float e = ex2_approx(2.0f * kLog2e * fabsf(y));
+  return copysignf(1.0f - __fdividef(2.0f, e + 1.0f), y);
+}
+// In place over N scores s: tanh(s * c). The polynomial serves a warp whose scores all stay
+// under half the cap (ordinary ones do); one exponential and one reciprocal each otherwise.
+// Rows that are not `live` hold anything and do not decide.
+template <int N>
+__device__ __forceinline__ void cap_scores(uint32_t (&r)[N], float c, bool live) {
+  float big = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; i += 2) big = fmax3(big, fabsf(__uint_as_float(r[i])), fabsf(__uint_as_float(r[i + 1])));
+  if (__all_sync(0xffffffffu, !live || big * fabsf(c) <= kTanhPolyLimit)) {
+    const unsigned long long c2 = f2_splat(c);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 t = f2_unpack(tanh_poly2(f2_mul(f2_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), c2)));
+      r[i] = __float_as_uint(t.x), r[i + 1] = __float_as_uint(t.y);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = __float_as_uint(tanh_exp(__uint_as_float(r[i]) * c));
+  }
+}
+
+}  // namespace wan
