@@ -70,7 +70,7 @@ int wan_attention_packed_fwd(const wan_dit_config* cfg, const wan_documents* doc
   PackedAttn p = make_packed(cfg, docs, q_rows, k_rows, kv_heads, q, k, v, o);
   p.lse = lse;
   if (cfg->dtype == WAN_BF16) return launch_attn_packed_tc(p, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
-  return launch_attn_packed_simt(p, cfg->dtype, static_cast<cudaStream_t>(stream));
+  return launch_attn_packed_simt(p, static_cast<cudaStream_t>(stream));
 }
 
 int wan_attention_packed_bwd(const wan_dit_config* cfg, const wan_documents* docs, int q_rows, int k_rows,
@@ -92,7 +92,7 @@ int wan_attention_packed_bwd(const wan_dit_config* cfg, const wan_documents* doc
   p.dq = dq->ptr, p.dk = dk->ptr, p.dv = dv->ptr;
   p.dq_stride = dq->row_stride, p.dk_stride = dk->row_stride, p.dv_stride = dv->row_stride;
   p.delta = static_cast<float*>(workspace);
-  return launch_attn_packed_simt_bwd(p, cfg->dtype, static_cast<cudaStream_t>(stream));
+  return launch_attn_packed_bwd(p, cfg->dtype, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

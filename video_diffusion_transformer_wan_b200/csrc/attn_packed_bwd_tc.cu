@@ -1,0 +1,628 @@
+// Gradient of the attention inside packed documents on the sm_100a tensor cores (bf16,
+// head_dim 128). With s the (capped, distance-biased) score, p = e^(s - lse) recomputed from
+// the stored log-sums, delta = sum(do * o) per row and turn = 1 - tanh^2 of a capped score:
+//   dp = do v^T,   ds = p (dp - delta) turn,
+//   dq = scale ds k,   dk = scale ds^T q,   dv = p^T do.
+//
+// Two kernels, one per side, so that every sum is formed in one place in a fixed order
+// (nothing is added across CTAs): 3 tile products a (query tile, key tile) for dq, 4 for
+// dk and dv, against 5 if one kernel did both and added dq through memory. p and ds are
+// rounded to bf16, the tensor cores' operand; everything else is fp32.
+//
+// A CTA owns 128 rows (packed query rows, or keys) and walks the tiles of the other side;
+// 384 threads, one CTA per SM: warp 0 loads by TMA, warp 1 issues tcgen05.mma, warp 2 (keys'
+// kernel) stages the per-query numbers, warp 3 clears ragged tiles, warps 4-11 do the scores:
+// a thread has half of a row's 128 columns (warps 4-7 the first, 8-11 the second).
+//   dq:  TMEM holds S twice, dP and dQ. While the score warps work on tile j the tensor core
+//        forms S(j+1), and dP(j+1) as soon as dP(j) is read; ds goes back over S(j) in bf16
+//        (each half into its own columns) as the A operand of dQ += ds K_j.
+//   dkv: the transposed scores, S^T = K Q^T and dP^T = V dO^T, so that p^T and ds^T are A
+//        operands too; both go back over S^T. TMEM holds S^T, dP^T, dV and dK: dP^T(i+1)
+//        overlaps the score warps, S^T(i+1) follows the products of tile i.
+// Rows behind a document's end belong to others: where they are summed over (K rows in dq; Q
+// and dO rows in dkv) they are cleared in shared memory, elsewhere masked or not stored.
+#include <math.h>
+
+#include <mutex>
+
+#include "internal.h"
+#include "packed_tc.cuh"
+
+namespace wan {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kScoreThreads = 256;
+constexpr int kDqStages = 5;
+constexpr int kDkvStages = 4;
+constexpr size_t kDqSmem = 1024 + static_cast<size_t>(kPkTileBytes) * (2 + kDqStages) + 512;
+// per staged query tile: float2 (log-sum, delta) or, with distances, float4 and a key count
+constexpr int kStatBytes = kPkTile * (16 + 4);
+constexpr size_t kDkvSmem = 1024 + static_cast<size_t>(kPkTileBytes) * (2 + kDkvStages) + 2 * kStatBytes + 512;
+static_assert(kDqSmem <= 232448 && kDkvSmem <= 232448, "shared memory of an SM");
+
+struct BwdParams {
+  PackedAttn a;
+  int pack, per_tile, groups;
+  float mult;      // log2 units per (possibly capped) score
+  float cap_in;    // scale / cap
+  int* err;
+};
+
+// This CTA's tile of documents' rows (found by warp 0); false past the last one.
+__device__ __forceinline__ bool cta_tile(const int32_t* cu, int n_docs, int rows, int per_tile, int* found, int& doc, int& tile) {
+  if (threadIdx.x < 32) {
+    int d = 0, t = 0;
+    const bool ok = find_doc_tile(cu, n_docs, rows, per_tile, blockIdx.x, d, t);
+    if (threadIdx.x == 0) found[0] = ok, found[1] = d, found[2] = t;
+  }
+  __syncthreads();
+  doc = found[1], tile = found[2];
+  return found[0] != 0;
+}
+
+// D (+)= A B over a 128-deep sum whose A halves lie at a and a + 64 columns in TMEM.
+__device__ __forceinline__ void mma_ts_halves(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool first) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    tc_mma_bf16_ts(d, a + (k >> 2) * 64 + (k & 3) * 8, b + ((k * 16 * 128) >> 4), idesc, (!first || k > 0) ? 1u : 0u);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t off = ((k >> 2) * kPkSpan + (k & 3) * 32) >> 4;
+    tc_mma_bf16(d, a + off, b + off, idesc, k > 0 ? 1u : 0u);
+  }
+}
+
+template <bool kPlain>
+__global__ void __launch_bounds__(kThreads, 1)
+    packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapO,
+                        const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
+                        const __grid_constant__ BwdParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;                      // Q, then dO
+  uint8_t* sKV = sQ + 2 * kPkTileBytes;    // [kDqStages]: K_0, V_0, K_1, V_1, ...
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + kDqStages * kPkTileBytes);
+  uint64_t* q_full = bars;
+  uint64_t* kv_full = bars + 1;
+  uint64_t* kv_empty = kv_full + kDqStages;
+  uint64_t* s_full = kv_empty + kDqStages;  // S(j) and dP(j) are there
+  uint64_t* y_free = s_full + 1;            // dP(j) has been read
+  uint64_t* ds_full = s_full + 2;
+  uint64_t* done = s_full + 3;
+  uint64_t* ragged = s_full + 4;
+  uint64_t* cleared = s_full + 5;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(s_full + 6);
+  int* found = reinterpret_cast<int*>(s_full + 7);
+
+  int di, tile;
+  if (!cta_tile(p.a.cu_q, p.a.n_docs, p.a.q_rows, p.per_tile, found, di, tile)) return;
+  const DocRows doc = load_doc(p.a, di);
+  tile = div_up(doc.Lq, p.per_tile) - 1 - tile;  // the tiles that see the most keys first
+  const int first = tile * p.per_tile, rows = min(p.per_tile, doc.Lq - first);
+  const int n = div_up(seen_keys(first + rows - 1, doc.off, doc.Lk, doc.prefix, p.a.causal_block), kPkTile);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    for (int s = 0; s < kDqStages; ++s) mbar_init(&kv_full[s], 1), mbar_init(&kv_empty[s], 1);
+    mbar_init(s_full, 1);
+    mbar_init(y_free, kScoreThreads);
+    mbar_init(ds_full, kScoreThreads);
+    mbar_init(done, 1);
+    mbar_init(ragged, 1);
+    mbar_init(cleared, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder, Y = tmem + 256, Z = tmem + 384;  // S(j) at tmem + 128 (j & 1)
+  const int end = doc.Lk - (n - 1) * kPkTile;  // keys of the last tile that are the document's
+
+  if (warp == 0) {
+    if (lane == 0 && n > 0) {
+      const uint32_t bytes = static_cast<uint32_t>(p.per_tile * p.pack) * 256u;
+      mbar_arrive_expect_tx(q_full, 2 * bytes);
+      for (int c = 0; c < 2; ++c) {
+        tma_load_3d(sQ + c * kPkSpan, &mapQ, q_full, 64 * c, blockIdx.y * p.pack, doc.q0 + first);
+        tma_load_3d(sQ + kPkTileBytes + c * kPkSpan, &mapO, q_full, 64 * c, blockIdx.y * p.pack, doc.q0 + first);
+      }
+      const int col = static_cast<int>(blockIdx.y) * p.pack / (p.a.H / p.a.Hk) * kPkD;
+      int issued = 0;
+      for (; issued < 2 * n; ++issued) {
+        const int stage = issued % kDqStages;
+        if (!mbar_wait(&kv_empty[stage], static_cast<uint32_t>((issued / kDqStages) & 1) ^ 1u, p.err)) break;
+        mbar_arrive_expect_tx(&kv_full[stage], kPkTileBytes);
+        for (int c = 0; c < 2; ++c)
+          tma_load_2d(sKV + stage * kPkTileBytes + c * kPkSpan, issued & 1 ? &mapV : &mapK, &kv_full[stage], col + 64 * c,
+                      doc.k0 + (issued >> 1) * kPkTile);
+      }
+      mbar_wait(q_full, 0, p.err);  // every copy this thread started has landed before it leaves
+      for (int s = 0; s < kDqStages; ++s) {
+        const int m = issued / kDqStages + (s < issued % kDqStages ? 1 : 0);
+        if (m > 0) mbar_wait(&kv_full[s], static_cast<uint32_t>((m - 1) & 1), p.err);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && n > 0) {
+      const uint32_t id_kk = idesc_bf16_f32(kPkTile, kPkTile, 0, 0), id_mn = idesc_bf16_f32(kPkTile, kPkD, 0, 1);
+      const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024), o_desc = sdesc_sw128(smem_u32(sQ + kPkTileBytes), 16, 1024);
+      const uint64_t kv_desc = sdesc_sw128(smem_u32(sKV), 16, 1024), kt_desc = sdesc_sw128(smem_u32(sKV), kPkSpan, 1024);
+      auto stage_off = [](int pos) { return static_cast<uint32_t>((pos % kDqStages * kPkTileBytes) >> 4); };
+      auto wait_pos = [&](int pos) {
+        return mbar_wait(&kv_full[pos % kDqStages], static_cast<uint32_t>((pos / kDqStages) & 1), p.err);
+      };
+      // S(j), then dP(j) once dP(j-1) has been read
+      auto scores = [&](int j) {
+        if (!wait_pos(2 * j)) return false;
+        if (j == n - 1 && end < kPkTile) {
+          mbar_arrive(ragged);
+          if (!mbar_wait(cleared, 0, p.err)) return false;
+        }
+        mma_ss(tmem + 128 * (j & 1), q_desc, kv_desc + stage_off(2 * j), id_kk);
+        if (!wait_pos(2 * j + 1)) return false;
+        if (j > 0 && !mbar_wait(y_free, static_cast<uint32_t>((j - 1) & 1), p.err)) return false;
+        tc_fence_after();
+        mma_ss(Y, o_desc, kv_desc + stage_off(2 * j + 1), id_kk);
+        tc_commit(&kv_empty[(2 * j + 1) % kDqStages]);
+        tc_commit(s_full);
+        return true;
+      };
+      bool ok = mbar_wait(q_full, 0, p.err) && scores(0);
+      for (int j = 0; ok && j < n; ++j) {
+        if (j + 1 < n && !scores(j + 1)) break;
+        if (!mbar_wait(ds_full, static_cast<uint32_t>(j & 1), p.err)) break;
+        tc_fence_after();
+        mma_ts_halves(Z, tmem + 128 * (j & 1), kt_desc + stage_off(2 * j), id_mn, j == 0);
+        tc_commit(&kv_empty[2 * j % kDqStages]);
+      }
+      tc_commit(done);
+      mbar_wait(done, 0, p.err);
+    }
+  } else if (warp == 3) {
+    if (n > 0 && end < kPkTile && mbar_wait_warp(ragged, 0, p.err)) {
+      zero_tile_rows(sKV + 2 * (n - 1) % kDqStages * kPkTileBytes, end);
+      if (lane == 0) mbar_arrive(cleared);
+    }
+  } else if (warp >= 4) {
+    const int half = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t at = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int query = row / p.pack, i = first + query, head = static_cast<int>(blockIdx.y) * p.pack + row - query * p.pack;
+    const bool live = query < rows;
+    const int seen = live ? seen_keys(i, doc.off, doc.Lk, doc.prefix, p.a.causal_block) : 0x7fffffff;
+    const int64_t stat = static_cast<int64_t>(head) * p.a.q_rows + doc.q0 + i;
+    const float nl = live ? -p.a.lse[stat] * kLog2e : 0.f, nd = live ? -p.a.delta[stat] : 0.f;
+    const float slope2 = !kPlain && p.a.slopes && live ? __ldg(p.a.slopes + head) * kLog2e : 0.f;
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      if (!mbar_wait_warp(s_full, static_cast<uint32_t>(j & 1), p.err)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t x = tmem + 128 * (j & 1) + at + 64 * half;
+      uint32_t s[64], g[64];
+      tmem_ld32(x, *reinterpret_cast<uint32_t(*)[32]>(s));
+      tmem_ld32(x + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+      tmem_ld32(Y + at + 64 * half, *reinterpret_cast<uint32_t(*)[32]>(g));
+      tmem_ld32(Y + at + 64 * half + 32, *reinterpret_cast<uint32_t(*)[32]>(g + 32));
+      tmem_ld_wait();
+      tc_fence_before();
+      mbar_arrive(y_free);
+      const int key0 = j * kPkTile + 64 * half;
+      const unsigned long long nl2 = f2_splat(nl), nd2 = f2_splat(nd), mult2 = f2_splat(p.mult);
+      if (!kPlain && p.a.cap > 0.f) {
+        cap_scores(s, p.cap_in, live);
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {  // g = (dp - delta)(1 - t^2)
+          const unsigned long long t = f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+          const unsigned long long d = f2_add(f2_pack(__uint_as_float(g[c]), __uint_as_float(g[c + 1])), nd2);
+          const float2 v = f2_unpack(f2_mul(d, f2_fma(f2_mul(t, f2_splat(-1.f)), t, f2_splat(1.f))));
+          g[c] = __float_as_uint(v.x), g[c + 1] = __float_as_uint(v.y);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          const float2 v = f2_unpack(f2_add(f2_pack(__uint_as_float(g[c]), __uint_as_float(g[c + 1])), nd2));
+          g[c] = __float_as_uint(v.x), g[c + 1] = __float_as_uint(v.y);
+        }
+      }
+      const float from = static_cast<float>(i + doc.off - key0);
+#pragma unroll
+      for (int c = 0; c < 64; c += 2) {
+        unsigned long long y = f2_fma(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), mult2, nl2);
+        if (!kPlain && p.a.slopes)
+          y = f2_add(y, f2_pack(-slope2 * fabsf(from - static_cast<float>(c)), -slope2 * fabsf(from - static_cast<float>(c + 1))));
+        const float2 e = f2_unpack(y);
+        const float2 d = f2_unpack(f2_mul(f2_pack(ex2_approx(e.x), ex2_approx(e.y)),
+                                          f2_pack(__uint_as_float(g[c]), __uint_as_float(g[c + 1]))));
+        s[c] = __float_as_uint(d.x), s[c + 1] = __float_as_uint(d.y);
+      }
+      const int valid = seen - key0;
+      if (__any_sync(0xffffffffu, valid < 64)) {
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+          if (c >= valid) s[c] = 0u;
+      }
+#pragma unroll
+      for (int c = 0; c < 32; ++c) s[c] = pack_bf16x2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
+      tmem_st32(x, *reinterpret_cast<uint32_t(*)[32]>(s));
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(ds_full);
+    }
+    if (ok && n > 0) ok = mbar_wait_warp(done, 0, p.err);
+    if (ok) {
+      tc_fence_after();
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.dq) + (static_cast<int64_t>(doc.q0) + i) * p.a.dq_stride + head * kPkD + 64 * half;
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
+        uint32_t r[32];
+        if (n > 0) {
+          tmem_ld32(Z + at + 64 * half + 32 * c, r);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int q = 0; q < 32; ++q) r[q] = 0u;
+        }
+        if (live) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint4 v;
+            v.x = pack_bf16x2(__uint_as_float(r[8 * q]) * p.a.scale, __uint_as_float(r[8 * q + 1]) * p.a.scale);
+            v.y = pack_bf16x2(__uint_as_float(r[8 * q + 2]) * p.a.scale, __uint_as_float(r[8 * q + 3]) * p.a.scale);
+            v.z = pack_bf16x2(__uint_as_float(r[8 * q + 4]) * p.a.scale, __uint_as_float(r[8 * q + 5]) * p.a.scale);
+            v.w = pack_bf16x2(__uint_as_float(r[8 * q + 6]) * p.a.scale, __uint_as_float(r[8 * q + 7]) * p.a.scale);
+            reinterpret_cast<uint4*>(out + c * 32)[q] = v;
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Query tiles of a document that see key tile `key0`, over the head groups of one key head:
+// tile i of the walk is query tile first_tile + i % per_group of group i / per_group.
+struct QueryWalk {
+  int first_tile, per_group, n;
+};
+__device__ __forceinline__ QueryWalk query_walk(const DocRows& d, const BwdParams& p, int key0) {
+  const int tiles = div_up(d.Lq, p.per_tile);
+  const int f = first_query(key0, d.off, d.Lk, d.prefix, p.a.causal_block) / p.per_tile;
+  const int per = f < tiles ? tiles - f : 0;
+  return {f, per, per * (p.a.H / p.a.Hk / p.pack)};
+}
+
+template <bool kPlain>
+__global__ void __launch_bounds__(kThreads, 1)
+    packed_dkv_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapO,
+                         const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
+                         const __grid_constant__ BwdParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sKV = smem;                      // K, then V
+  uint8_t* sQ = sKV + 2 * kPkTileBytes;     // [kDkvStages]: Q_0, dO_0, Q_1, dO_1, ...
+  uint8_t* stats = sQ + kDkvStages * kPkTileBytes;  // [2] per query: -log-sum, -delta (, slope, position), then keys seen
+  uint64_t* bars = reinterpret_cast<uint64_t*>(stats + 2 * kStatBytes);
+  uint64_t* kv_full = bars;
+  uint64_t* q_full = bars + 1;
+  uint64_t* q_empty = q_full + kDkvStages;
+  uint64_t* s_full = q_empty + kDkvStages;
+  uint64_t* y_free = s_full + 1;
+  uint64_t* p_full = s_full + 2;            // p^T and ds^T are in place
+  uint64_t* done = s_full + 3;
+  uint64_t* ragged = s_full + 4;
+  uint64_t* cleared = s_full + 5;
+  uint64_t* st_full = s_full + 6;           // [2]
+  uint64_t* st_empty = s_full + 8;          // [2]
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(s_full + 10);
+  int* found = reinterpret_cast<int*>(s_full + 11);
+
+  int di, tile;
+  if (!cta_tile(p.a.cu_k, p.a.n_docs, p.a.k_rows, kPkTile, found, di, tile)) return;
+  const DocRows doc = load_doc(p.a, di);
+  const int key0 = tile * kPkTile, keys = min(kPkTile, doc.Lk - key0);
+  const QueryWalk w = query_walk(doc, p, key0);
+  const int used = p.per_tile * p.pack;     // rows of a tile that are queries
+  const int last_rows = (doc.Lq - (div_up(doc.Lq, p.per_tile) - 1) * p.per_tile) * p.pack;  // of a document's last tile
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(kv_full, 1);
+    for (int s = 0; s < kDkvStages; ++s) mbar_init(&q_full[s], 1), mbar_init(&q_empty[s], 1);
+    mbar_init(s_full, 1);
+    mbar_init(y_free, kScoreThreads);
+    mbar_init(p_full, kScoreThreads);
+    mbar_init(done, 1);
+    mbar_init(ragged, 1);
+    mbar_init(cleared, 1);
+    for (int b = 0; b < 2; ++b) mbar_init(&st_full[b], 1), mbar_init(&st_empty[b], kScoreThreads);
+    fence_mbar_init();
+  }
+  // Rows that no copy writes take part in the sums over queries.
+  if (used < kPkTile && warp >= 4 && warp < 4 + kDkvStages) zero_tile_rows(sQ + (warp - 4) * kPkTileBytes, used);
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder, Y = tmem + 128, dV = tmem + 256, dK = tmem + 384;
+  const int hk = blockIdx.y, group0 = hk * (p.a.H / p.a.Hk / p.pack);
+
+  if (warp == 0) {
+    if (lane == 0 && w.n > 0) {
+      mbar_arrive_expect_tx(kv_full, 2 * kPkTileBytes);
+      for (int c = 0; c < 2; ++c) {
+        tma_load_2d(sKV + c * kPkSpan, &mapK, kv_full, hk * kPkD + 64 * c, doc.k0 + key0);
+        tma_load_2d(sKV + kPkTileBytes + c * kPkSpan, &mapV, kv_full, hk * kPkD + 64 * c, doc.k0 + key0);
+      }
+      int issued = 0;
+      for (; issued < 2 * w.n; ++issued) {
+        const int stage = issued % kDkvStages, i = issued >> 1, g = i / w.per_group;
+        if (!mbar_wait(&q_empty[stage], static_cast<uint32_t>((issued / kDkvStages) & 1) ^ 1u, p.err)) break;
+        mbar_arrive_expect_tx(&q_full[stage], static_cast<uint32_t>(used) * 256u);
+        for (int c = 0; c < 2; ++c)
+          tma_load_3d(sQ + stage * kPkTileBytes + c * kPkSpan, issued & 1 ? &mapO : &mapQ, &q_full[stage], 64 * c,
+                      (group0 + g) * p.pack, doc.q0 + (w.first_tile + i - g * w.per_group) * p.per_tile);
+      }
+      mbar_wait(kv_full, 0, p.err);  // every copy this thread started has landed before it leaves
+      for (int s = 0; s < kDkvStages; ++s) {
+        const int m = issued / kDkvStages + (s < issued % kDkvStages ? 1 : 0);
+        if (m > 0) mbar_wait(&q_full[s], static_cast<uint32_t>((m - 1) & 1), p.err);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && w.n > 0) {
+      const uint32_t id_kk = idesc_bf16_f32(kPkTile, kPkTile, 0, 0), id_mn = idesc_bf16_f32(kPkTile, kPkD, 0, 1);
+      const uint64_t k_desc = sdesc_sw128(smem_u32(sKV), 16, 1024), v_desc = sdesc_sw128(smem_u32(sKV + kPkTileBytes), 16, 1024);
+      const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024), qt_desc = sdesc_sw128(smem_u32(sQ), kPkSpan, 1024);
+      auto stage_off = [](int pos) { return static_cast<uint32_t>((pos % kDkvStages * kPkTileBytes) >> 4); };
+      auto wait_pos = [&](int pos) {
+        return mbar_wait(&q_full[pos % kDkvStages], static_cast<uint32_t>((pos / kDkvStages) & 1), p.err);
+      };
+      int ragged_seen = 0;
+      // Tile i is there, its rows behind the document's end cleared.
+      auto arrived = [&](int i) {
+        if (!wait_pos(2 * i) || !wait_pos(2 * i + 1)) return false;
+        if (last_rows < used && (i + 1) % w.per_group == 0) {
+          mbar_arrive(ragged);
+          if (!mbar_wait(cleared, static_cast<uint32_t>(ragged_seen++ & 1), p.err)) return false;
+        }
+        return true;
+      };
+      bool ok = mbar_wait(kv_full, 0, p.err) && arrived(0);
+      if (ok) {
+        mma_ss(tmem, k_desc, q_desc + stage_off(0), id_kk);
+        mma_ss(Y, v_desc, q_desc + stage_off(1), id_kk);
+        tc_commit(s_full);
+      }
+      for (int i = 0; ok && i < w.n; ++i) {
+        if (i + 1 < w.n) {
+          if (!arrived(i + 1) || !mbar_wait(y_free, static_cast<uint32_t>(i & 1), p.err)) break;
+          tc_fence_after();
+          mma_ss(Y, v_desc, q_desc + stage_off(2 * i + 3), id_kk);
+        }
+        if (!mbar_wait(p_full, static_cast<uint32_t>(i & 1), p.err)) break;
+        tc_fence_after();
+        mma_ts_halves(dV, tmem, qt_desc + stage_off(2 * i + 1), id_mn, i == 0);
+        tc_commit(&q_empty[(2 * i + 1) % kDkvStages]);
+        mma_ts_halves(dK, tmem + 32, qt_desc + stage_off(2 * i), id_mn, i == 0);
+        tc_commit(&q_empty[2 * i % kDkvStages]);
+        if (i + 1 < w.n) {
+          mma_ss(tmem, k_desc, q_desc + stage_off(2 * i + 2), id_kk);
+          tc_commit(s_full);
+        }
+      }
+      tc_commit(done);
+      mbar_wait(done, 0, p.err);
+    }
+  } else if (warp == 2) {
+    // The numbers of each query tile's columns. A column of no query, and a query that sees
+    // nothing, get p = 2^(s - infinity) = 0.
+    for (int i = 0; i < w.n; ++i) {
+      const int b = i & 1, g = i / w.per_group;
+      if (i >= 2 && !mbar_wait_warp(&st_empty[b], static_cast<uint32_t>(((i >> 1) - 1) & 1), p.err)) break;
+      uint8_t* st = stats + b * kStatBytes;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int m = c * 32 + lane, qi = m / p.pack, head = (group0 + g) * p.pack + m - qi * p.pack;
+        const int q = (w.first_tile + i - g * w.per_group) * p.per_tile + qi;
+        const bool live = qi < p.per_tile && q < doc.Lq;
+        float nl = -INFINITY, nd = 0.f, slope2 = 0.f;
+        int seen = 0;
+        if (live) {
+          const int64_t stat = static_cast<int64_t>(head) * p.a.q_rows + doc.q0 + q;
+          const float lse = p.a.lse[stat];
+          if (lse != -INFINITY) nl = -lse * kLog2e, nd = -p.a.delta[stat];
+          seen = seen_keys(q, doc.off, doc.Lk, doc.prefix, p.a.causal_block);
+          if (!kPlain && p.a.slopes) slope2 = __ldg(p.a.slopes + head) * kLog2e;
+        }
+        if (kPlain)
+          reinterpret_cast<float2*>(st)[m] = make_float2(nl, nd);
+        else
+          reinterpret_cast<float4*>(st)[m] = make_float4(nl, nd, slope2, static_cast<float>(q + doc.off - key0));
+        reinterpret_cast<int*>(st + kPkTile * 16)[m] = seen;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&st_full[b]);
+    }
+  } else if (warp == 3) {
+    if (last_rows < used) {
+      int k = 0;
+      for (int i = w.per_group - 1; w.per_group > 0 && i < w.n; i += w.per_group, ++k) {
+        if (!mbar_wait_warp(ragged, static_cast<uint32_t>(k & 1), p.err)) break;
+        zero_tile_rows(sQ + 2 * i % kDkvStages * kPkTileBytes, last_rows);
+        zero_tile_rows(sQ + (2 * i + 1) % kDkvStages * kPkTileBytes, last_rows);
+        if (lane == 0) mbar_arrive(cleared);
+      }
+    }
+  } else {
+    const int half = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t at = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t x = tmem + at + 64 * half;
+    const bool live = row < keys;
+    bool ok = true;
+    for (int i = 0; i < w.n; ++i) {
+      const int b = i & 1;
+      if (!mbar_wait_warp(&st_full[b], static_cast<uint32_t>((i >> 1) & 1), p.err) ||
+          !mbar_wait_warp(s_full, static_cast<uint32_t>(i & 1), p.err)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      uint32_t s[64], g[64];
+      tmem_ld32(x, *reinterpret_cast<uint32_t(*)[32]>(s));
+      tmem_ld32(x + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+      tmem_ld32(Y + at + 64 * half, *reinterpret_cast<uint32_t(*)[32]>(g));
+      tmem_ld32(Y + at + 64 * half + 32, *reinterpret_cast<uint32_t(*)[32]>(g + 32));
+      tmem_ld_wait();
+      tc_fence_before();
+      mbar_arrive(y_free);
+      const uint8_t* st = stats + b * kStatBytes;
+      if (!kPlain && p.a.cap > 0.f) cap_scores(s, p.cap_in, live);
+      const unsigned long long mult2 = f2_splat(p.mult);
+      const float key = static_cast<float>(row);
+#pragma unroll
+      for (int c = 0; c < 64; c += 2) {
+        float2 nl, nd;
+        const unsigned long long t = f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+        if constexpr (kPlain) {
+          const float4 v = reinterpret_cast<const float4*>(st)[32 * half + (c >> 1)];
+          nl = make_float2(v.x, v.z), nd = make_float2(v.y, v.w);
+        } else {
+          const float4 v0 = reinterpret_cast<const float4*>(st)[64 * half + c], v1 = reinterpret_cast<const float4*>(st)[64 * half + c + 1];
+          nl = make_float2(v0.x - v0.z * fabsf(v0.w - key), v1.x - v1.z * fabsf(v1.w - key)), nd = make_float2(v0.y, v1.y);
+        }
+        const float2 e = f2_unpack(f2_fma(t, mult2, f2_pack(nl.x, nl.y)));
+        unsigned long long d = f2_add(f2_pack(__uint_as_float(g[c]), __uint_as_float(g[c + 1])), f2_pack(nd.x, nd.y));
+        if (!kPlain && p.a.cap > 0.f) d = f2_mul(d, f2_fma(f2_mul(t, f2_splat(-1.f)), t, f2_splat(1.f)));
+        const float e0 = ex2_approx(e.x), e1 = ex2_approx(e.y);
+        const float2 v = f2_unpack(f2_mul(f2_pack(e0, e1), d));
+        s[c] = __float_as_uint(e0), s[c + 1] = __float_as_uint(e1);
+        g[c] = __float_as_uint(v.x), g[c + 1] = __float_as_uint(v.y);
+      }
+      if (p.a.causal_block > 0) {
+        // queries see ever more keys: the tile's first column decides whether any is masked
+        const int* seen = reinterpret_cast<const int*>(st + kPkTile * 16);
+        if (seen[0] < key0 + keys) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (key0 + row >= seen[64 * half + c]) s[c] = 0u, g[c] = 0u;
+        }
+      }
+      mbar_arrive(&st_empty[b]);
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        s[c] = pack_bf16x2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
+        g[c] = pack_bf16x2(__uint_as_float(g[2 * c]), __uint_as_float(g[2 * c + 1]));
+      }
+      tmem_st32(x, *reinterpret_cast<uint32_t(*)[32]>(s));
+      tmem_st32(x + 32, *reinterpret_cast<uint32_t(*)[32]>(g));
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(p_full);
+    }
+    if (ok && w.n > 0) ok = mbar_wait_warp(done, 0, p.err);
+    if (ok) {
+      tc_fence_after();
+      const int64_t key_row = static_cast<int64_t>(doc.k0) + key0 + row;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {  // two quarters of dV, two of dK
+        uint32_t r[32];
+        const int col = 64 * half + 32 * (c & 1);
+        if (w.n > 0) {
+          tmem_ld32((c < 2 ? dV : dK) + at + col, r);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int q = 0; q < 32; ++q) r[q] = 0u;
+        }
+        if (live) {
+          const float f = c < 2 ? 1.0f : p.a.scale;
+          __nv_bfloat16* out = c < 2 ? static_cast<__nv_bfloat16*>(p.a.dv) + key_row * p.a.dv_stride
+                                     : static_cast<__nv_bfloat16*>(p.a.dk) + key_row * p.a.dk_stride;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint4 v;
+            v.x = pack_bf16x2(__uint_as_float(r[8 * q]) * f, __uint_as_float(r[8 * q + 1]) * f);
+            v.y = pack_bf16x2(__uint_as_float(r[8 * q + 2]) * f, __uint_as_float(r[8 * q + 3]) * f);
+            v.z = pack_bf16x2(__uint_as_float(r[8 * q + 4]) * f, __uint_as_float(r[8 * q + 5]) * f);
+            v.w = pack_bf16x2(__uint_as_float(r[8 * q + 6]) * f, __uint_as_float(r[8 * q + 7]) * f);
+            reinterpret_cast<uint4*>(out + hk * kPkD + col)[q] = v;
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace
+
+int launch_attn_packed_tc_bwd(const PackedAttn& a, cudaStream_t s) {
+  BwdParams p{};
+  p.a = a;
+  p.pack = packed_heads_per_tile(a.H, a.Hk);
+  p.per_tile = kPkTile / p.pack;
+  p.groups = a.H / p.pack;
+  p.mult = (a.cap > 0.f ? a.cap : a.scale) * kLog2e;
+  p.cap_in = a.cap > 0.f ? a.scale / a.cap : 0.f;
+  p.err = device_error_flag();
+  int dev = 0;
+  cudaGetDevice(&dev);
+  static std::once_flag once[64];
+  std::call_once(once[dev & 63], [] {
+    for (auto kernel : {packed_dq_tc_kernel<true>, packed_dq_tc_kernel<false>})
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kDqSmem));
+    for (auto kernel : {packed_dkv_tc_kernel<true>, packed_dkv_tc_kernel<false>})
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kDkvSmem));
+  });
+  CUtensorMap mq, mo, mk, mv;
+  // without queries (or keys) none is loaded: any valid map will do
+  const bool qs = a.q_rows > 0, ks = a.k_rows > 0;
+  if (!make_packed_kv_map(&mk, ks ? a.k : a.q, ks ? a.k_stride : a.q_stride, ks ? a.k_rows : 1, a.Hk) ||
+      !make_packed_kv_map(&mv, ks ? a.v : a.q, ks ? a.v_stride : a.q_stride, ks ? a.k_rows : 1, a.Hk))
+    return WAN_ERR_CUDA;
+  if (!qs) {
+    mq = mo = mk;
+  } else if (!make_packed_q_map(&mq, a.q, a.q_stride, a.q_rows, a.H, p.pack) ||
+             !make_packed_q_map(&mo, a.d_o, a.do_stride, a.q_rows, a.H, p.pack)) {
+    return WAN_ERR_CUDA;
+  }
+  const bool plain = a.cap == 0.f && !a.slopes;
+  // every document adds less than one partial tile
+  if (qs) {
+    const dim3 grid(static_cast<unsigned>(a.q_rows / p.per_tile + a.n_docs), static_cast<unsigned>(p.groups));
+    (plain ? packed_dq_tc_kernel<true> : packed_dq_tc_kernel<false>)<<<grid, kThreads, kDqSmem, s>>>(mq, mo, mk, mv, p);
+    count_launches(1);
+    const int st = check_launch();
+    if (st != WAN_OK) return st;
+  }
+  if (ks) {
+    const dim3 grid(static_cast<unsigned>(a.k_rows / kPkTile + a.n_docs), static_cast<unsigned>(a.Hk));
+    (plain ? packed_dkv_tc_kernel<true> : packed_dkv_tc_kernel<false>)<<<grid, kThreads, kDkvSmem, s>>>(mq, mo, mk, mv, p);
+    count_launches(1);
+    return check_launch();
+  }
+  return WAN_OK;
+}
+
+}  // namespace wan

@@ -282,13 +282,19 @@ int fwd(const PackedAttn& p, cudaStream_t s) {
   return check_launch();
 }
 template <typename T>
+int delta(const PackedAttn& p, cudaStream_t s) {
+  if (p.q_rows == 0) {
+    count_launches(-1);
+    return WAN_OK;
+  }
+  const int64_t warps = static_cast<int64_t>(p.q_rows) * p.H;
+  packed_delta_kernel<T><<<static_cast<unsigned>((warps + 7) / 8), 256, 0, s>>>(p);
+  return check_launch();
+}
+template <typename T>
 int bwd(const PackedAttn& p, cudaStream_t s) {
   int st = WAN_OK;
   if (p.q_rows > 0) {
-    const int64_t warps = static_cast<int64_t>(p.q_rows) * p.H;
-    packed_delta_kernel<T><<<static_cast<unsigned>((warps + 7) / 8), 256, 0, s>>>(p);
-    st = check_launch();
-    if (st != WAN_OK) return st;
     const size_t sm = tile_bytes(p.d, 4, 1);
     allow_smem(packed_dq_kernel<T>, sm);
     packed_dq_kernel<T><<<dim3(most_tiles(p.q_rows, p.n_docs), p.H), kThreads, sm, s>>>(p);
@@ -307,16 +313,17 @@ int bwd(const PackedAttn& p, cudaStream_t s) {
 
 }  // namespace
 
-int launch_attn_packed_simt(const PackedAttn& p, int dtype, cudaStream_t s) {
+int launch_attn_packed_simt(const PackedAttn& p, cudaStream_t s) {
   trace_launch_begin(WAN_KIND_ATTN, s);
-  const int st = dtype == WAN_BF16 ? fwd<__nv_bfloat16>(p, s) : fwd<float>(p, s);
+  const int st = fwd<float>(p, s);
   trace_launch_end(WAN_KIND_ATTN, s);
   return st;
 }
 
-int launch_attn_packed_simt_bwd(const PackedAttn& p, int dtype, cudaStream_t s) {
+int launch_attn_packed_bwd(const PackedAttn& p, int dtype, cudaStream_t s) {
   trace_launch_begin(WAN_KIND_ATTN, s);
-  const int st = dtype == WAN_BF16 ? bwd<__nv_bfloat16>(p, s) : bwd<float>(p, s);
+  int st = dtype == WAN_BF16 ? delta<__nv_bfloat16>(p, s) : delta<float>(p, s);
+  if (st == WAN_OK) st = dtype == WAN_BF16 ? launch_attn_packed_tc_bwd(p, s) : bwd<float>(p, s);
   trace_launch_end(WAN_KIND_ATTN, s);
   return st;
 }

@@ -183,9 +183,11 @@ size_t attn_packed_tc_workspace(const PackedAttn& p);
 int packed_heads_per_tile(int H, int Hk);
 bool make_packed_q_map(CUtensorMap* map, const void* ptr, int64_t stride, int rows, int H, int pack);
 bool make_packed_kv_map(CUtensorMap* map, const void* ptr, int64_t stride, int rows, int Hk);
-// CUDA cores, fp32 arithmetic, head_dim <= 128 (act = dtype).
-int launch_attn_packed_simt(const PackedAttn& p, int dtype, cudaStream_t s);
-int launch_attn_packed_simt_bwd(const PackedAttn& p, int dtype, cudaStream_t s);
+// The gradient's tensor-core kernels (delta already formed).
+int launch_attn_packed_tc_bwd(const PackedAttn& p, cudaStream_t s);
+// fp32 on the CUDA cores, head_dim <= 128; and the whole gradient of either type.
+int launch_attn_packed_simt(const PackedAttn& p, cudaStream_t s);
+int launch_attn_packed_bwd(const PackedAttn& p, int dtype, cudaStream_t s);
 
 // Small kernels.
 int launch_patch_gather(const void* latent, int B, int C, int F, int H, int W, void* patches, int dtype,
