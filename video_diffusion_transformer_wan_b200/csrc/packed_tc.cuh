@@ -45,12 +45,6 @@ __device__ __forceinline__ void zero_tile_rows(uint8_t* tile, int row0) {
 // tanh on the FMA pipes for |y| <= 1/2: an odd polynomial fitted for least largest error of
 // tanh(y)/y on that range (1.3e-8; 2^-24 absolute with its fp32 roundings).
 constexpr float kTanhPolyLimit = 0.5f;
-__device__ __forceinline__ unsigned long long f2_mul(unsigned long long a, unsigned long long b) {
-  unsigned long long r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ unsigned long long f2_splat(float v) { return f2_pack(v, v); }
 __device__ __forceinline__ unsigned long long tanh_poly2(unsigned long long y) {
   const unsigned long long z = f2_mul(y, y);
   unsigned long long p = f2_fma(f2_splat(0.017151299864053726f), z, f2_splat(-0.05299423262476921f));

@@ -211,24 +211,54 @@ __global__ void __launch_bounds__(kMaxThreads) gated_residual_norm_kernel(const 
   }
 }
 
+// The gradient's statistics with one barrier for both norms: sums that would need the row's mean
+// first are taken about the warp's own mean and moved to the row's. Every warp leaves its
+// sums, every lane then takes one warp's; rows alternate between two halves.
+struct RowSums {
+  float4 x[2][32];   // columns, their sum, squares about the warp's mean (RMS: about 0)
+  float2 xg[2][32];  // sums of dn (x - the warp's mean) and of dn
+  float4 y[2][32];
+  float2 k[2][32];
+};
+
+__device__ __forceinline__ void ask_l2(const void* at) { asm volatile("prefetch.global.L2 [%0];" ::"l"(at)); }
+
+// The row's mean (0 for RMS), r, and sums of g (v - mean) and g, from the warps' (lane w: warp w).
+__device__ __forceinline__ void join_warps(float4 s, float2 g, int kind, float inv_d, float eps, float& mean, float& r,
+                                           float& a, float& b) {
+  mean = kind == WAN_NORM_LAYER ? warp_sum(s.y) * inv_d : 0.f;
+  const float own = kind == WAN_NORM_LAYER && s.x > 0.f ? s.y / s.x : 0.f, off = own - mean;
+  const float m2 = warp_sum(fmaf(s.x * off, off, s.z));
+  r = rsqrtf(fmaf(m2, inv_d, eps));
+  a = warp_sum(fmaf(g.y, off, g.x));
+  b = warp_sum(g.y);
+}
+
 template <typename T, int NU, int kMaxThreads>
 __global__ void __launch_bounds__(kMaxThreads) gated_residual_norm_bwd_kernel(const ResNormParams p) {
-  __shared__ float buf[2][32][2];
-  int half = 0;
-  const int tpr = blockDim.x;
+  __shared__ RowSums sm;
+  const int tpr = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int col[NU];
   bool on[NU];
+  float mine = 0.f;  // columns of this thread
 #pragma unroll
   for (int u = 0; u < NU; ++u) {
     col[u] = (u * tpr + threadIdx.x) * 8;
     on[u] = col[u] < p.D;
+    mine += on[u] ? 8.f : 0.f;
   }
+  const float warp_cols = warp_sum(mine), inv_cols = warp_cols > 0.f ? 1.0f / warp_cols : 0.f;
   const float inv_d = 1.0f / static_cast<float>(p.D);
+  for (int i = threadIdx.x; i < 64; i += tpr) {  // entries of absent warps stay 0
+    sm.x[0][i] = sm.y[0][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    sm.xg[0][i] = sm.k[0][i] = make_float2(0.f, 0.f);
+  }
+  __syncthreads();
   const RowSpan span = block_rows(p, blockIdx.x, gridDim.x);
   if (span.lo >= span.hi) return;
   float g[NU][8], sc[NU][8];                      // gate w_post; w (1 + scale)
   float s0[NU][8] = {}, s1[NU][8] = {}, s2[NU][8] = {};
-  int doc = -1;
+  int doc = -1, half = 0;
   int64_t doc_end = -1;
   auto flush = [&]() {
     if (!p.part) return;
@@ -244,18 +274,25 @@ __global__ void __launch_bounds__(kMaxThreads) gated_residual_norm_bwd_kernel(co
       for (int i = 0; i < 8; ++i) s0[u][i] = s1[u][i] = s2[u][i] = 0.f;
     }
   };
-  for (int64_t row = span.lo; row < span.hi; ++row) {
-    float n[NU][8], y[NU][8], dh[NU][8], G[NU][8];
+  for (int64_t row = span.lo; row < span.hi; ++row, half ^= 1) {
+    float x[NU][8], y[NU][8], dh[NU][8];
+    Raw8<float> rg[NU];
     {
-      Raw8<float> rn[NU], rg[NU];
+      Raw8<float> rx[NU];
       Raw8<T> ry[NU], rh[NU];
 #pragma unroll
       for (int u = 0; u < NU; ++u)
         if (on[u]) {
-          load_raw8(rn[u], p.x + row * p.D + col[u]);
+          load_raw8(rx[u], p.x + row * p.D + col[u]);
           load_raw8(rh[u], static_cast<const T*>(p.dh) + row * p.D + col[u]);
           load_raw8(ry[u], static_cast<const T*>(p.y) + row * p.D + col[u]);
           if (p.dx_out) load_raw8(rg[u], p.dx_out + row * p.D + col[u]);
+          if (row + 1 < span.hi) {  // the next row on its way into L2
+            ask_l2(p.x + (row + 1) * p.D + col[u]);
+            ask_l2(static_cast<const T*>(p.dh) + (row + 1) * p.D + col[u]);
+            ask_l2(static_cast<const T*>(p.y) + (row + 1) * p.D + col[u]);
+            if (p.dx_out) ask_l2(p.dx_out + (row + 1) * p.D + col[u]);
+          }
         }
       if (row >= doc_end) {
         if (doc >= 0) flush();
@@ -274,79 +311,108 @@ __global__ void __launch_bounds__(kMaxThreads) gated_residual_norm_bwd_kernel(co
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
         if (on[u]) {
-          unpack8(rn[u], n[u]);
+          unpack8(rx[u], x[u]);
           unpack8(rh[u], dh[u]);
           unpack8(ry[u], y[u]);
-          if (p.dx_out) unpack8(rg[u], G[u]);
-        }
-        if (!on[u] || !p.dx_out)
+          if (!p.dx_out) rg[u] = Raw8<float>{};
+        } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            G[u][i] = 0.f;
-            if (!on[u]) n[u][i] = dh[u][i] = y[u][i] = 0.f;
-          }
+          for (int i = 0; i < 8; ++i) x[u][i] = dh[u][i] = y[u][i] = g[u][i] = sc[u][i] = 0.f;
+          rg[u] = Raw8<float>{};
+        }
       }
     }
-    const float r = normalise<NU>(n, on, p.pre, inv_d, p.eps, buf, half);
-    float m[2] = {0.f, 0.f};  // sums of dn n and dn
+    // This warp's sums: of x about its own mean, with dn = dh sc, and of y.
+    float sum = 0.f, own = 0.f, m2 = 0.f, ga = 0.f, gb = 0.f;
+    if (p.pre == WAN_NORM_LAYER) {
+#pragma unroll
+      for (int u = 0; u < NU; ++u)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += x[u][i];
+      sum = warp_sum(sum);
+      own = sum * inv_cols;
+    }
 #pragma unroll
     for (int u = 0; u < NU; ++u)
       if (on[u])
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          s0[u][i] += dh[u][i];
-          s1[u][i] = fmaf(dh[u][i], n[u][i], s1[u][i]);
-          dh[u][i] *= sc[u][i];
-          m[0] = fmaf(dh[u][i], n[u][i], m[0]);
-          m[1] += dh[u][i];
+          const float v = x[u][i] - own, dn = dh[u][i] * sc[u][i];
+          m2 = fmaf(v, v, m2);
+          ga = fmaf(dn, v, ga);
+          gb += dn;
         }
-    block_sums<2>(m, buf, half);
-    const float a = m[0] * inv_d, c = p.pre == WAN_NORM_LAYER ? m[1] * inv_d : 0.f;
+    m2 = warp_sum(m2), ga = warp_sum(ga), gb = warp_sum(gb);
+    float ysum = 0.f, yown = 0.f, ym2 = 0.f;
+    if (p.post != WAN_NORM_NONE) {
+      if (p.post == WAN_NORM_LAYER) {
 #pragma unroll
-    for (int u = 0; u < NU; ++u)
-      if (on[u]) {
-        float dx[8];
+        for (int u = 0; u < NU; ++u)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          G[u][i] = fmaf(r, dh[u][i] - c - n[u][i] * a, G[u][i]);
-          dx[i] = p.residual_scale * G[u][i];
-        }
-        store_vec8(p.dx + row * p.D + col[u], dx);
+          for (int i = 0; i < 8; ++i) ysum += y[u][i];
+        ysum = warp_sum(ysum);
+        yown = ysum * inv_cols;
       }
-    if (p.post == WAN_NORM_NONE) {
-#pragma unroll
-      for (int u = 0; u < NU; ++u)
-        if (on[u]) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            s2[u][i] = fmaf(G[u][i], y[u][i], s2[u][i]);
-            y[u][i] = G[u][i] * g[u][i];
-          }
-          store_vec8(static_cast<T*>(p.dy) + row * p.D + col[u], y[u]);
-        }
-    } else {
-      const float ry = normalise<NU>(y, on, p.post, inv_d, p.eps, buf, half);
-      float k[2] = {0.f, 0.f};
 #pragma unroll
       for (int u = 0; u < NU; ++u)
         if (on[u])
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            s2[u][i] = fmaf(G[u][i], y[u][i], s2[u][i]);
-            G[u][i] *= g[u][i];
-            k[0] = fmaf(G[u][i], y[u][i], k[0]);
-            k[1] += G[u][i];
-          }
-      block_sums<2>(k, buf, half);
-      const float ka = k[0] * inv_d, kc = p.post == WAN_NORM_LAYER ? k[1] * inv_d : 0.f;
-#pragma unroll
-      for (int u = 0; u < NU; ++u)
-        if (on[u]) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[u][i] = ry * (G[u][i] - kc - y[u][i] * ka);
-          store_vec8(static_cast<T*>(p.dy) + row * p.D + col[u], y[u]);
-        }
+          for (int i = 0; i < 8; ++i) ym2 = fmaf(y[u][i] - yown, y[u][i] - yown, ym2);
+      ym2 = warp_sum(ym2);
     }
+    if (lane == 0) {
+      sm.x[half][warp] = make_float4(warp_cols, sum, m2, 0.f);
+      sm.xg[half][warp] = make_float2(ga, gb);
+      sm.y[half][warp] = make_float4(warp_cols, ysum, ym2, 0.f);
+    }
+    __syncthreads();
+    float mean, r, a, c;
+    join_warps(sm.x[half][lane], sm.xg[half][lane], p.pre, inv_d, p.eps, mean, r, a, c);
+    // dn n sums to a r; G = dx_out + r (dn - [mean dn] - n mean(dn n))
+    a *= r * r * inv_d;
+    c = p.pre == WAN_NORM_LAYER ? c * inv_d : 0.f;
+    float ymean = 0.f, ry = 1.f;
+    if (p.post != WAN_NORM_NONE) {
+      float d0, d1;
+      join_warps(sm.y[half][lane], make_float2(0.f, 0.f), p.post, inv_d, p.eps, ymean, ry, d0, d1);
+    }
+    float k0 = 0.f, k1 = 0.f;
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+      if (on[u]) {
+        float gv[8], dx[8];
+        unpack8(rg[u], gv);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float v = x[u][i] - mean;
+          s0[u][i] += dh[u][i];
+          s1[u][i] = fmaf(dh[u][i], v * r, s1[u][i]);
+          const float G = fmaf(r, fmaf(dh[u][i], sc[u][i], -c) - v * a, gv[i]);
+          dx[i] = p.residual_scale * G;
+          y[u][i] = (y[u][i] - ymean) * ry;
+          s2[u][i] = fmaf(G, y[u][i], s2[u][i]);
+          x[u][i] = G * g[u][i];
+          k0 = fmaf(x[u][i], y[u][i], k0);
+          k1 += x[u][i];
+        }
+        store_vec8(p.dx + row * p.D + col[u], dx);
+      }
+    float ka = 0.f, kc = 0.f;
+    if (p.post != WAN_NORM_NONE) {
+      k0 = warp_sum(k0), k1 = warp_sum(k1);
+      if (lane == 0) sm.k[half][warp] = make_float2(k0, k1);
+      __syncthreads();
+      const float2 k = sm.k[half][lane];
+      ka = warp_sum(k.x) * inv_d;
+      kc = p.post == WAN_NORM_LAYER ? warp_sum(k.y) * inv_d : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+      if (on[u]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[u][i] = ry * (x[u][i] - kc - y[u][i] * ka);
+        store_vec8(static_cast<T*>(p.dy) + row * p.D + col[u], y[u]);
+      }
   }
   flush();
 }
@@ -472,7 +538,7 @@ int run_bwd(const ResNormParams& p, const wan_residual_norm_grads& g, float* tot
   int blocks = 0, st = WAN_OK;
   if (p.n_docs > 0)
     st = p.D <= 2048 ? launch_bwd<T, 1, 256>(p, s, &blocks)
-                     : p.D <= 5120 ? launch_bwd<T, 2, 320>(p, s, &blocks) : launch_bwd<T, 2, 512>(p, s, &blocks);
+                     : p.D <= 5120 ? launch_bwd<T, 1, 640>(p, s, &blocks) : launch_bwd<T, 2, 512>(p, s, &blocks);
   if (st != WAN_OK || !p.part) return st;
   if (p.n_docs > 0) {
     const int docs_y = p.n_docs < 1024 ? p.n_docs : 1024;

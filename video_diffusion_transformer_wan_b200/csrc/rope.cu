@@ -6,13 +6,18 @@
 // gives dx = r (g w - x r^2 m) and dw = sum over rows of g x r.
 //
 // HBM-bound: the forward reads and writes every element once, the gradient reads two and
-// writes one. A half-warp holds one head of one row, 8 elements (four whole pairs) a lane,
-// so a rotation needs no exchange: with interleaved pairs a lane owns 8 consecutive
-// elements, with split halves 4 of each half. A block takes `tb` rows and holds NI heads
-// per half-warp in registers; all its loads are issued before anything waits, and the
-// cosines are made while they fly: one (row, pair) each, shared by all heads of q and k
-// through shared memory, the angle reduced in fp64 (positions may be far), the sine in
-// fp32. The width norm adds one exchange of the heads' partial sums through shared memory.
+// writes one; what has to be kept down is the instructions per element and what warps wait
+// for. A warp of qk_norm_rope_kernel takes a row of q or of k by itself, a lane 8 columns (four
+// whole pairs: 8 neighbours, or 4 of each half) of every 256, the same place in every head: its
+// cosines serve all heads, sums are shuffles, and no warp waits for another. (Blocks that
+// shared a row, a thread for the same columns of every row, spent 4 times the instructions on
+// exchanges and waited at barriers: 108 us against 75 us forward, 179 against 154 us gradient, on
+// 32,760 and 27,569 rows of 12 + 12 heads.) The cosines of a row are made once per pair, the
+// turns reduced in fp64 (positions may be far) and the sine taken in fp32. Up to 6 x 256 columns
+// of a side stay in registers between the norm's sums and their use; wider rows are read
+// twice, the second time from the caches.
+// qk_norm_rope_any_kernel serves what this layout does not divide: rows that are not 16-byte
+// aligned, heads that do not divide 256 dims or are below 8, halves of odd quads.
 #include <cuda_bf16.h>
 
 #include <math.h>
@@ -20,6 +25,7 @@
 #include "checks.h"
 #include "internal.h"
 #include "packed.cuh"
+#include "ptx.cuh"
 
 namespace wan {
 namespace {
@@ -37,85 +43,12 @@ struct RopeParams {
   const int32_t* pos;
   int rows, H, n, d, tb, norm, layout, pairs, n_axes;  // n = heads of q and k together
   float eps, amplitude;
-  double freq[kMaxPairs];
+  double freq[kMaxPairs];  // turns per position: frequency / 2 pi
   uint8_t axis[kMaxPairs];
 };
 
-// A lane's four pairs. V = 4: two quads of elements (16-byte accesses where the quads are
-// neighbours); V = 1: single elements, for shapes that quads do not divide.
-template <int V>
-struct Lane;
-template <>
-struct Lane<4> {
-  int da, db, p0;  // first elements of the quads; first pair (or -1: the quads only pass)
-  bool on, split;  // split: pair k is (da + k, db + k); else (da + 2k, da + 2k + 1) over both quads
-  __device__ Lane(const RopeParams& p, int u) {
-    split = false;
-    if (p.layout == WAN_ROPE_HALF) {
-      const int turning = p.pairs >> 2;
-      split = u < turning;
-      da = split ? 4 * u : 2 * p.pairs + 8 * (u - turning);
-      db = split ? 4 * u + p.pairs : da + 4;
-      p0 = split ? 4 * u : -1;
-    } else {
-      da = 8 * u, db = da + 4, p0 = 4 * u;
-    }
-    on = 8 * u < p.d;
-  }
-  __device__ __forceinline__ int pair(int k) const { return p0 < 0 ? kMaxPairs : p0 + k; }
-  __device__ __forceinline__ void load(Raw8<__nv_bfloat16>& r, const __nv_bfloat16* x) const {
-    if (!on) {
-      r.u = make_uint4(0, 0, 0, 0);
-    } else if (split) {
-      const uint2 a = __ldcs(reinterpret_cast<const uint2*>(x + da)), b = __ldcs(reinterpret_cast<const uint2*>(x + db));
-      r.u = make_uint4(a.x, a.y, b.x, b.y);
-    } else {
-      load_raw8(r, x + da);
-    }
-  }
-  __device__ __forceinline__ void load(Raw8<float>& r, const float* x) const {
-    if (!on) {
-      r.a = r.b = make_float4(0, 0, 0, 0);
-    } else {
-      r.a = __ldcs(reinterpret_cast<const float4*>(x + da));
-      r.b = __ldcs(reinterpret_cast<const float4*>(x + db));
-    }
-  }
-  template <typename T>
-  __device__ __forceinline__ void pairs_of(const Raw8<T>& r, float (&a)[4], float (&b)[4]) const {
-    float v[8];
-    unpack8(r, v);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) a[k] = split ? v[k] : v[2 * k], b[k] = split ? v[4 + k] : v[2 * k + 1];
-  }
-  __device__ __forceinline__ void join(const float (&a)[4], const float (&b)[4], float (&v)[8]) const {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[k] = split ? a[k] : ((k & 1) ? b[k >> 1] : a[k >> 1]);
-      v[4 + k] = split ? b[k] : ((k & 1) ? b[2 + (k >> 1)] : a[2 + (k >> 1)]);
-    }
-  }
-  __device__ __forceinline__ void store(__nv_bfloat16* x, const float (&a)[4], const float (&b)[4]) const {
-    if (!on) return;
-    float v[8];
-    join(a, b, v);
-    if (split) {
-      *reinterpret_cast<uint2*>(x + da) = make_uint2(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]));
-      *reinterpret_cast<uint2*>(x + db) = make_uint2(pack2_bf16(v[4], v[5]), pack2_bf16(v[6], v[7]));
-    } else {
-      store_vec8(x + da, v);
-    }
-  }
-  __device__ __forceinline__ void store(float* x, const float (&a)[4], const float (&b)[4]) const {
-    if (!on) return;
-    float v[8];
-    join(a, b, v);
-    *reinterpret_cast<float4*>(x + da) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4*>(x + db) = make_float4(v[4], v[5], v[6], v[7]);
-  }
-};
-template <>
-struct Lane<1> {
+// A lane's pairs u, u + 16, ..., element by element.
+struct Lane {
   int u, d, n_pairs;
   bool half;
   __device__ Lane(const RopeParams& p, int lane)
@@ -167,13 +100,21 @@ __device__ __forceinline__ float sum16(float v) {
   return v;
 }
 
-template <typename T, int V, int NI, bool kBwd>
-__global__ void __launch_bounds__(256) qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
+// amplitude (cos, sin) of the angle of position * freq turns.
+__device__ __forceinline__ float2 turn(int pos, double freq, float amplitude) {
+  const double turns = static_cast<double>(pos) * freq;
+  float s, c;
+  sincospif(2.0f * static_cast<float>(turns - rint(turns)), &s, &c);
+  return make_float2(c * amplitude, s * amplitude);
+}
+
+template <typename T, int NI, bool kBwd>
+__global__ void __launch_bounds__(256) qk_norm_rope_any_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kHw = 16;  // half-warps per block
   __shared__ float2 cs[kMaxTb][kMaxPairs + 1];  // the last entry: no turn (1, 0)
   __shared__ float red[kBwd ? 2 : 1][kHw * NI];
   const int hw = threadIdx.x >> 4, u = threadIdx.x & 15;
-  const Lane<V> lane(p, u);
+  const Lane lane(p, u);
   const int items = p.tb * p.n;
   if (threadIdx.x < kMaxTb) cs[threadIdx.x][kMaxPairs] = make_float2(1.f, 0.f);
   float dw[kBwd ? NI : 1][8] = {};
@@ -201,11 +142,7 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const __grid_constant
     for (int w = threadIdx.x; w < p.tb * p.pairs; w += 256) {
       const int t = w / p.pairs, j = w - t * p.pairs;
       if (row0 + t < p.rows) {
-        const double angle = static_cast<double>(p.pos[(row0 + t) * p.n_axes + p.axis[j]]) * p.freq[j];
-        const double turns = rint(angle * 0.15915494309189535);  // 1 / (2 pi)
-        float s, c;
-        sincosf(static_cast<float>(fma(turns, -6.283185307179586, angle)), &s, &c);
-        cs[t][j] = make_float2(c * p.amplitude, s * p.amplitude);
+        cs[t][j] = turn(p.pos[(row0 + t) * p.n_axes + p.axis[j]], p.freq[j], p.amplitude);
       }
     }
     __syncthreads();
@@ -320,27 +257,360 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const __grid_constant
   }
 }
 
-// dw[col] = sum over blocks, their rows and (per-head norm) heads of the partial sums, in a
-// fixed order: thread row y takes every 32nd summand, the 32 partial sums are added in
-// shared memory. blockIdx.y: q or k.
-__global__ void __launch_bounds__(1024) rope_dw_kernel(const float* __restrict__ part, int blocks, int tb, int n, int H,
-                                                       int d, bool per_head, float* dw_q, float* dw_k) {
+using F2 = unsigned long long;  // two fp32
+
+constexpr int kMaxHeads = 96;  // q and k heads of one row together
+constexpr int kWarps = 8;      // per block
+constexpr int kHeld = 6;       // groups of 256 columns that stay in registers
+
+// A thread's 8 columns of a head: two quads at da and db; pairs (da + 2k, da + 2k + 1), or,
+// split, (da + k, db + k).
+template <bool kHalf>
+struct Cols {
+  int da, db, quad;  // quad: entry of the cosine table (16: the columns only pass)
+  bool on, split;
+  __device__ Cols(const RopeParams& p, int u) {
+    on = 8 * u < p.d;
+    const int turning = p.pairs >> 2;
+    split = kHalf && u < turning;
+    if (kHalf) {
+      da = split ? 4 * u : 2 * p.pairs + 8 * (u - turning);
+      db = split ? 4 * u + p.pairs : da + 4;
+      quad = split ? u : 16;
+    } else {
+      da = 8 * u, db = da + 4, quad = u;
+    }
+  }
+  __device__ __forceinline__ void load(Raw8<__nv_bfloat16>& r, const __nv_bfloat16* x) const {
+    if (kHalf) {
+      const uint2 a = __ldcs(reinterpret_cast<const uint2*>(x + da)), b = __ldcs(reinterpret_cast<const uint2*>(x + db));
+      r.u = make_uint4(a.x, a.y, b.x, b.y);
+    } else {
+      load_raw8(r, x + da);
+    }
+  }
+  __device__ __forceinline__ void load(Raw8<float>& r, const float* x) const {
+    r.a = __ldcs(reinterpret_cast<const float4*>(x + da));
+    r.b = __ldcs(reinterpret_cast<const float4*>(x + db));
+  }
+  // The first and second parts of the four pairs, two to a register pair (of passing columns:
+  // any order, the inverse of `store`).
+  template <typename T>
+  __device__ __forceinline__ void pairs_of(const Raw8<T>& r, F2 (&a)[2], F2 (&b)[2]) const {
+    float v[8];
+    unpack8(r, v);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      a[k] = kHalf ? f2_pack(v[2 * k], v[2 * k + 1]) : f2_pack(v[4 * k], v[4 * k + 2]);
+      b[k] = kHalf ? f2_pack(v[4 + 2 * k], v[5 + 2 * k]) : f2_pack(v[4 * k + 1], v[4 * k + 3]);
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(T* x, const F2 (&a2)[2], const F2 (&b2)[2]) const {
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float2 a = f2_unpack(a2[k]), b = f2_unpack(b2[k]);
+      v[kHalf ? 2 * k : 4 * k] = a.x, v[kHalf ? 2 * k + 1 : 4 * k + 2] = a.y;
+      v[kHalf ? 4 + 2 * k : 4 * k + 1] = b.x, v[kHalf ? 5 + 2 * k : 4 * k + 3] = b.y;
+    }
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(x + da) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(x + db) = make_float4(v[4], v[5], v[6], v[7]);
+    } else if (kHalf) {
+      *reinterpret_cast<uint2*>(x + da) = make_uint2(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]));
+      *reinterpret_cast<uint2*>(x + db) = make_uint2(pack2_bf16(v[4], v[5]), pack2_bf16(v[6], v[7]));
+    } else {
+      store_vec8(x + da, v);
+    }
+  }
+};
+
+// A turn's cosines, sines and negated sines of a thread's four pairs.
+struct Turns {
+  F2 c[2], s[2], ns[2];
+  __device__ __forceinline__ Turns(const float4& co, const float4& si) {
+    c[0] = f2_pack(co.x, co.y), c[1] = f2_pack(co.z, co.w), s[0] = f2_pack(si.x, si.y), s[1] = f2_pack(si.z, si.w);
+    ns[0] = f2_pack(-si.x, -si.y), ns[1] = f2_pack(-si.z, -si.w);
+  }
+};
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float sum_of(F2 v) {
+  const float2 f = f2_unpack(v);
+  return f.x + f.y;
+}
+
+// Four pairs as two float4, `apart` float4 from one another.
+__device__ __forceinline__ void put_pairs(float4* at, int apart, const F2 (&a)[2], const F2 (&b)[2]) {
+  *reinterpret_cast<ulonglong2*>(at) = make_ulonglong2(a[0], a[1]);
+  *reinterpret_cast<ulonglong2*>(at + apart) = make_ulonglong2(b[0], b[1]);
+}
+__device__ __forceinline__ void get_pairs(const float4* at, int apart, F2 (&a)[2], F2 (&b)[2]) {
+  const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(at), y = *reinterpret_cast<const ulonglong2*>(at + apart);
+  a[0] = x.x, a[1] = x.y, b[0] = y.x, b[1] = y.y;
+}
+
+// One side's rows: q (blocks [0, q_blocks)) or k (the others), a warp each, in turn. CH: groups
+// of 256 columns held in registers; 0: any number, read twice. Dynamic shared memory, fp32: the
+// weights, then (gradient) each warp's sums of their gradients, both in the order in which
+// lanes take them (four first parts of pairs per lane, then, from chunks * 128 on, the
+// second parts), so that they move in 16 bytes without conflicts.
+template <typename T, int CH, bool kHalf, bool kBwd>
+__global__ void __launch_bounds__(kWarps * 32, kBwd && CH > 0 ? 2 : 1) qk_norm_rope_kernel(const __grid_constant__ RopeParams p, int q_blocks) {
+  extern __shared__ float4 dyn[];
+  __shared__ float4 cosv[kWarps][17], sinv[kWarps][17];  // entry 16: no turn
+  const bool is_q = static_cast<int>(blockIdx.x) < q_blocks;
+  const int block = is_q ? blockIdx.x : blockIdx.x - q_blocks, blocks = is_q ? q_blocks : gridDim.x - q_blocks;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int W = (is_q ? p.H : p.n - p.H) * p.d, groups = (W + 255) / 256, chunks = CH > 0 ? CH : groups;
+  const Cols<kHalf> cols(p, lane * 8 % p.d / 8);
+  const int head0 = lane * 8 / p.d * p.d;  // the lane's head in a group of 256 columns
+  const bool normed = p.norm != WAN_QK_NORM_NONE;
+  float4* w_sm = dyn;                                            // [2][groups][32]
+  float4* dw_sm = dyn + (normed ? groups * 64 * (1 + warp) : 0);  // the same for each warp
+  auto on = [&](int c) { return c * 256 + lane * 8 < W; };
+  if (normed) {
+    const T* w = static_cast<const T*>(is_q ? p.w_q : p.w_k);
+    for (int c = warp; c < groups; c += kWarps) {
+      F2 a[2] = {}, b[2] = {};
+      if (on(c)) {
+        Raw8<T> r;
+        cols.load(r, w + (p.norm == WAN_QK_NORM_WIDTH ? c * 256 + head0 : 0));
+        cols.pairs_of(r, a, b);
+      }
+      put_pairs(w_sm + c * 32 + lane, groups * 32, a, b);
+    }
+    if (kBwd)
+      for (int i = lane; i < groups * 64; i += 32) dw_sm[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  for (int i = lane; i < 17; i += 32) cosv[warp][i] = make_float4(1.f, 1.f, 1.f, 1.f), sinv[warp][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  __syncthreads();
+  const int j1 = lane + 32 < p.pairs ? lane + 32 : 0;
+  const double freq0 = p.pairs > 0 && lane < p.pairs ? p.freq[lane] : 0.0, freq1 = p.freq[j1];
+  const int axis0 = lane < p.pairs ? p.axis[lane] : 0, axis1 = p.axis[j1];
+  const T* in = static_cast<const T*>(is_q ? p.q_in : p.k_in);
+  const T* grad = static_cast<const T*>(is_q ? p.gq : p.gk);
+  T* out = static_cast<T*>(is_q ? p.q_out : p.k_out);
+  const int64_t in_stride = is_q ? p.q_stride : p.k_stride, g_stride = is_q ? p.gq_stride : p.gk_stride;
+  const int64_t out_stride = is_q ? p.qo_stride : p.ko_stride;
+  const float inv_d = 1.0f / p.d, inv_w = 1.0f / W;
+  const int lanes = p.d / 8;
+  auto head_sum = [&](float v) {
+    for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  };
+
+  // The next positions are read a row ahead. The gradient, whose registers leave only 16 warps
+  // an SM, asks rows into L2 two ahead (201 us without, 164 one ahead, 154 two; the forward
+  // gains nothing from it).
+  const int64_t step = static_cast<int64_t>(blocks) * kWarps;
+  auto ask = [&](const T* base, int64_t stride, int64_t row) {
+    const char* line = reinterpret_cast<const char*>(base + row * stride);
+    for (int i = lane * 128; i < W * static_cast<int>(sizeof(T)); i += 4096)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(line + i));
+  };
+  int64_t row = static_cast<int64_t>(block) * kWarps + warp;
+  int pos0 = 0, pos1 = 0;
+  auto read_pos = [&](int64_t at) {
+    if (at >= p.rows) return;
+    pos0 = __ldg(p.pos + at * p.n_axes + axis0);
+    pos1 = __ldg(p.pos + at * p.n_axes + axis1);
+  };
+  read_pos(row);
+  for (; row < p.rows; row += step) {
+    const T* xr = in + row * in_stride + head0;
+    const T* gr = grad + row * g_stride + head0;
+    T* orow = out + row * out_stride + head0;
+    Raw8<T> rx[CH > 0 ? CH : 1], rg[CH > 0 && kBwd ? CH : 1];
+    if constexpr (CH > 0) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        if (on(c)) {
+          if (!kBwd || normed) cols.load(rx[c], xr + c * 256);
+          if constexpr (kBwd) cols.load(rg[c], gr + c * 256);
+        } else {
+          rx[c] = Raw8<T>{};
+          if constexpr (kBwd) rg[c] = Raw8<T>{};
+        }
+      }
+    }
+    if (kBwd && row + 2 * step < p.rows) {
+      if (normed) ask(in, in_stride, row + 2 * step);
+      ask(grad, g_stride, row + 2 * step);
+    }
+    {
+      float2 t = turn(pos0, freq0, p.amplitude);
+      if (lane < p.pairs) reinterpret_cast<float*>(cosv[warp])[lane] = t.x, reinterpret_cast<float*>(sinv[warp])[lane] = t.y;
+      if (p.pairs > 32) {
+        t = turn(pos1, freq1, p.amplitude);
+        if (lane + 32 < p.pairs) reinterpret_cast<float*>(cosv[warp])[lane + 32] = t.x, reinterpret_cast<float*>(sinv[warp])[lane + 32] = t.y;
+      }
+    }
+    read_pos(row + step);
+    __syncwarp();
+    const Turns w(cosv[warp][cols.quad], sinv[warp][cols.quad]);
+    __syncwarp();  // read before the next row's are written
+    // The columns of group c: input pairs, and, for the gradient, the turned-back gradient.
+    auto x_of = [&](int c, F2 (&a)[2], F2 (&b)[2]) {
+      Raw8<T> r{};
+      if constexpr (CH > 0)
+        r = rx[c];
+      else if (on(c) && (!kBwd || normed))
+        cols.load(r, xr + c * 256);
+      cols.pairs_of(r, a, b);
+    };
+    auto turn_back = [&](const Raw8<T>& r, F2 (&ga)[2], F2 (&gb)[2]) {
+      F2 a[2], b[2];
+      cols.pairs_of(r, a, b);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        ga[k] = f2_fma(a[k], w.c[k], f2_mul(b[k], w.s[k]));
+        gb[k] = f2_fma(b[k], w.c[k], f2_mul(a[k], w.ns[k]));
+      }
+    };
+    F2 ha[CH > 0 && kBwd ? CH : 1][2], hb[CH > 0 && kBwd ? CH : 1][2];  // the turned gradient, held
+    if constexpr (CH > 0 && kBwd) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) turn_back(rg[c], ha[c], hb[c]);
+    }
+    auto g_of = [&](int c, F2 (&ga)[2], F2 (&gb)[2]) {
+      if constexpr (CH > 0 && kBwd) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) ga[k] = ha[c][k], gb[k] = hb[c][k];
+      } else {
+        Raw8<T> r{};
+        if (on(c)) cols.load(r, gr + c * 256);
+        turn_back(r, ga, gb);
+      }
+    };
+    auto w_of = [&](int c, F2 (&a)[2], F2 (&b)[2]) {
+      if (CH > 0 && c >= groups) {
+        a[0] = a[1] = b[0] = b[1] = 0ull;
+      } else {
+        get_pairs(w_sm + c * 32 + lane, groups * 32, a, b);
+      }
+    };
+    // Sums of x^2 and g w x over group c.
+    auto sums = [&](int c, float& s, float& m) {
+      F2 xa[2], xb[2];
+      x_of(c, xa, xb);
+      s = sum_of(f2_fma(xa[0], xa[0], f2_fma(xb[0], xb[0], f2_fma(xa[1], xa[1], f2_mul(xb[1], xb[1])))));
+      m = 0.f;
+      if constexpr (kBwd) {
+        F2 ga[2], gb[2], wa[2], wb[2];
+        g_of(c, ga, gb);
+        w_of(c, wa, wb);
+        F2 v = f2_mul(f2_mul(ga[0], wa[0]), xa[0]);
+        v = f2_fma(f2_mul(gb[0], wb[0]), xb[0], v);
+        v = f2_fma(f2_mul(ga[1], wa[1]), xa[1], v);
+        m = sum_of(f2_fma(f2_mul(gb[1], wb[1]), xb[1], v));
+      }
+    };
+    float r = 1.f, mean = 0.f;
+    if (p.norm == WAN_QK_NORM_WIDTH) {
+      float s = 0.f, m = 0.f;
+#pragma unroll
+      for (int c = 0; c < chunks; ++c) {
+        float sc, mc;
+        sums(c, sc, mc);
+        s += sc, m += mc;
+      }
+      r = rsqrtf(fmaf(warp_sum(s), inv_w, p.eps));
+      if (kBwd) mean = warp_sum(m) * inv_w;
+    }
+#pragma unroll
+    for (int c = 0; c < chunks; ++c) {
+      if (p.norm == WAN_QK_NORM_HEAD) {
+        float s, m;
+        sums(c, s, m);
+        r = rsqrtf(fmaf(head_sum(s), inv_d, p.eps));
+        if (kBwd) mean = head_sum(m) * inv_d;
+      }
+      F2 oa[2], ob[2], xa[2], xb[2], wa[2], wb[2];
+      if (!kBwd || normed) x_of(c, xa, xb);
+      if (normed) w_of(c, wa, wb);
+      if constexpr (!kBwd) {
+        if (normed) {
+          const F2 r2 = f2_splat(r);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) xa[k] = f2_mul(xa[k], f2_mul(r2, wa[k])), xb[k] = f2_mul(xb[k], f2_mul(r2, wb[k]));
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          oa[k] = f2_fma(xa[k], w.c[k], f2_mul(xb[k], w.ns[k]));
+          ob[k] = f2_fma(xa[k], w.s[k], f2_mul(xb[k], w.c[k]));
+        }
+      } else {
+        F2 ga[2], gb[2];
+        g_of(c, ga, gb);
+        if (normed) {
+          // xh = x r:  dx = g r w - xh r^2 mean,  dw += g xh
+          const F2 r2 = f2_splat(r), f = f2_splat(-r * r * mean);
+          float4* mine = dw_sm + c * 32 + lane;
+          F2 da[2], db[2];
+          if (CH == 0 || c < groups) get_pairs(mine, groups * 32, da, db);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            xa[k] = f2_mul(xa[k], r2), xb[k] = f2_mul(xb[k], r2);
+            da[k] = f2_fma(ga[k], xa[k], da[k]), db[k] = f2_fma(gb[k], xb[k], db[k]);
+            oa[k] = f2_fma(xa[k], f, f2_mul(ga[k], f2_mul(r2, wa[k])));
+            ob[k] = f2_fma(xb[k], f, f2_mul(gb[k], f2_mul(r2, wb[k])));
+          }
+          if (CH == 0 || c < groups) put_pairs(mine, groups * 32, da, db);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) oa[k] = ga[k], ob[k] = gb[k];
+        }
+      }
+      if (on(c)) cols.store(orow + c * 256, oa, ob);
+    }
+  }
+  if constexpr (kBwd) {
+    if (!normed) return;
+    __syncthreads();
+    // The block's sums, warp after warp, back in the columns' order.
+    float* part = p.part + (is_q ? static_cast<int64_t>(block) * W : static_cast<int64_t>(q_blocks) * p.H * p.d + static_cast<int64_t>(block) * W);
+    for (int c = warp; c < groups; c += kWarps) {
+      F2 a[2] = {}, b[2] = {};
+      for (int v = 0; v < kWarps; ++v) {
+        F2 x[2], y[2];
+        get_pairs(dyn + groups * 64 * (1 + v) + c * 32 + lane, groups * 32, x, y);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) a[k] = f2_add(a[k], x[k]), b[k] = f2_add(b[k], y[k]);
+      }
+      if (on(c)) cols.store(part + c * 256 + head0, a, b);
+    }
+  }
+}
+
+// dw[col] = sum over partial rows and (per-head norm) heads, in a fixed order: thread row y
+// takes every 32nd summand, the 32 partial sums are added in shared memory. blockIdx.y: q or k,
+// whose partial rows begin at part + at and lie `pitch` apart.
+struct DwSide {
+  int64_t at;
+  int rows, heads;
+  float* out;
+};
+__global__ void __launch_bounds__(1024) rope_dw_kernel(const float* __restrict__ part, DwSide q, DwSide k, int64_t pitch_q,
+                                                       int64_t pitch_k, int d, bool per_head) {
   __shared__ float acc[32][33];
-  const bool is_q = blockIdx.y == 0;
-  float* out = is_q ? dw_q : dw_k;
-  const int h0 = is_q ? 0 : H, heads = is_q ? H : n - H;
-  const int cols = per_head ? d : heads * d;
-  if (!out || static_cast<int>(blockIdx.x) * 32 >= cols) return;
+  const DwSide side = blockIdx.y == 0 ? q : k;
+  const int64_t pitch = blockIdx.y == 0 ? pitch_q : pitch_k;
+  const int cols = per_head ? d : side.heads * d;
+  if (!side.out || static_cast<int>(blockIdx.x) * 32 >= cols) return;
   const int col = blockIdx.x * 32 + threadIdx.x;
   float s = 0.f;
   if (col < cols) {
-    const int hs = per_head ? heads : 1;
-    const int64_t count = static_cast<int64_t>(blocks) * tb * hs;
-    const int first = h0 * d + col;
+    const int hs = per_head ? side.heads : 1;
+    for (int h = 0; h < hs; ++h) {
+      const float* first = part + side.at + h * d + col;
 #pragma unroll 4
-    for (int64_t i = threadIdx.y; i < count; i += 32) {
-      const int64_t bt = i / hs;
-      s += part[bt * n * d + (i - bt * hs) * d + first];
+      for (int i = threadIdx.y; i < side.rows; i += 32) s += first[i * pitch];
     }
   }
   acc[threadIdx.y][threadIdx.x] = s;
@@ -349,17 +619,18 @@ __global__ void __launch_bounds__(1024) rope_dw_kernel(const float* __restrict__
     float v = 0.f;
 #pragma unroll
     for (int y = 0; y < 32; ++y) v += acc[y][threadIdx.x];
-    out[col] = v;
+    side.out[col] = v;
   }
 }
 
-// Heads per half-warp and rows per block. Few rows: one row a block, the most blocks;
-// else the split that leaves the fewest idle half-warps, the larger one of equals.
+// Blocks of one launch; any_kernel: heads per half-warp, rows per block; the other: blocks of q.
 struct RopePlan {
-  int ni, tb, blocks;
+  int ni, tb, blocks, q_blocks;
 };
-RopePlan plan_rope(int rows, int n, bool dw) {
-  RopePlan best{(n + 15) / 16, 1, rows};
+// Few rows: one row a block, the most blocks; else the split that leaves the fewest idle
+// half-warps, the larger one of equals.
+RopePlan plan_any(int rows, int n, bool dw) {
+  RopePlan best{(n + 15) / 16, 1, rows, 0};
   if (rows > 2 * 148) {
     float most = 0.f;
     for (int ni = (n + 15) / 16; ni <= 6; ++ni) {
@@ -372,26 +643,61 @@ RopePlan plan_rope(int rows, int n, bool dw) {
   if (dw && best.blocks > kDwBlocks) best.blocks = kDwBlocks;
   return best;
 }
-
-template <typename T, int V, int NI, bool kBwd>
-int launch_ni(const RopeParams& p, int blocks, cudaStream_t s) {
-  qk_norm_rope_kernel<T, V, NI, kBwd><<<static_cast<unsigned>(blocks), 256, 0, s>>>(p);
+template <typename T, int NI, bool kBwd>
+int launch_any(const RopeParams& p, const RopePlan& pl, cudaStream_t s) {
+  qk_norm_rope_any_kernel<T, NI, kBwd><<<static_cast<unsigned>(pl.blocks), 256, 0, s>>>(p);
   return check_launch();
 }
-template <typename T, int V, bool kBwd>
-int launch_v(const RopeParams& p, const RopePlan& pl, cudaStream_t s) {
+template <typename T, bool kBwd>
+int run_any(const RopeParams& p, const RopePlan& pl, cudaStream_t s) {
   switch (pl.ni) {
-    case 1: return launch_ni<T, V, 1, kBwd>(p, pl.blocks, s);
-    case 2: return launch_ni<T, V, 2, kBwd>(p, pl.blocks, s);
-    case 3: return launch_ni<T, V, 3, kBwd>(p, pl.blocks, s);
-    case 4: return launch_ni<T, V, 4, kBwd>(p, pl.blocks, s);
-    case 5: return launch_ni<T, V, 5, kBwd>(p, pl.blocks, s);
-    case 6: return launch_ni<T, V, 6, kBwd>(p, pl.blocks, s);
+    case 1: return launch_any<T, 1, kBwd>(p, pl, s);
+    case 2: return launch_any<T, 2, kBwd>(p, pl, s);
+    case 3: return launch_any<T, 3, kBwd>(p, pl, s);
+    case 4: return launch_any<T, 4, kBwd>(p, pl, s);
+    case 5: return launch_any<T, 5, kBwd>(p, pl, s);
+    case 6: return launch_any<T, 6, kBwd>(p, pl, s);
   }
   return WAN_ERR_UNSUPPORTED;
 }
 
-constexpr int kMaxHeads = 96;  // q and k heads of one row together (six per half-warp)
+// Dynamic shared memory of one block (see the kernel).
+size_t vec_smem(const RopeParams& p, bool bwd) {
+  if (p.norm == WAN_QK_NORM_NONE) return 0;
+  const size_t widest = static_cast<size_t>(p.H > p.n - p.H ? p.H : p.n - p.H) * p.d;
+  return (widest + 255) / 256 * 1024 * (bwd ? 1 + kWarps : 1);
+}
+// As many blocks as are resident at once, no more than rows need, shared out between q and k
+// by their widths. The weights' gradients take one partial row per block, for which the
+// workspace has kDwBlocks.
+template <typename T, int CH, bool kHalf, bool kBwd>
+int launch_vec(const RopeParams& p, RopePlan& pl, bool dw, cudaStream_t s) {
+  auto kernel = qk_norm_rope_kernel<T, CH, kHalf, kBwd>;
+  const size_t smem = vec_smem(p, kBwd);
+  int dev = 0, sms = 0, per_sm = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (smem > 40 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kWarps * 32, smem);
+  int most = (sms > 0 ? sms : 148) * (per_sm > 0 ? per_sm : 1);
+  if (dw && most > kDwBlocks) most = kDwBlocks;
+  const int need = (p.rows + kWarps - 1) / kWarps;  // of each side
+  pl.q_blocks = static_cast<int>(static_cast<int64_t>(most) * p.H / p.n);
+  pl.q_blocks = pl.q_blocks < 1 ? 1 : (pl.q_blocks < need ? pl.q_blocks : need);
+  int k_blocks = 0;
+  if (p.n > p.H) {
+    k_blocks = most - pl.q_blocks;
+    k_blocks = k_blocks < 1 ? 1 : (k_blocks < need ? k_blocks : need);
+  }
+  pl.blocks = pl.q_blocks + k_blocks;
+  kernel<<<static_cast<unsigned>(pl.blocks), kWarps * 32, smem, s>>>(p, pl.q_blocks);
+  return check_launch();
+}
+template <typename T, bool kHalf, bool kBwd>
+int run_vec(const RopeParams& p, RopePlan& pl, bool dw, cudaStream_t s) {
+  const int widest = (p.H > p.n - p.H ? p.H : p.n - p.H) * p.d;
+  return widest <= kHeld * 256 ? launch_vec<T, kHeld, kHalf, kBwd>(p, pl, dw, s) : launch_vec<T, 0, kHalf, kBwd>(p, pl, dw, s);
+}
 
 int check_rope(const wan_rope* r, int head_dim) {
   WAN_REQUIRE(r, WAN_ERR_NULL);
@@ -426,7 +732,7 @@ void fill_frequencies(const wan_rope* r, RopeParams& p) {
         const double keep = fmin(1.0, fmax(0.0, (turns - r->slow) / (r->fast - r->slow)));
         f *= keep + (1.0 - keep) / r->factor[a];
       }
-      p.freq[p.pairs] = f;
+      p.freq[p.pairs] = f / 6.283185307179586;
       p.axis[p.pairs++] = static_cast<uint8_t>(a);
     }
   }
@@ -448,18 +754,26 @@ int check_common(const wan_dit_config* cfg, const wan_rope* rope, const int32_t*
   return WAN_OK;
 }
 
+template <typename T, bool kBwd>
+int run_typed(RopeParams& p, bool vec, bool dw, RopePlan& pl, cudaStream_t s) {
+  if (!vec) {
+    pl = plan_any(p.rows, p.n, dw);
+    p.tb = pl.tb;
+    return run_any<T, kBwd>(p, pl, s);
+  }
+  return p.layout == WAN_ROPE_HALF ? run_vec<T, true, kBwd>(p, pl, dw, s) : run_vec<T, false, kBwd>(p, pl, dw, s);
+}
 template <bool kBwd>
-int run_rope(const wan_dit_config* cfg, RopeParams& p, bool vec, bool dw, cudaStream_t s) {
-  const RopePlan pl = plan_rope(p.rows, p.n, dw);
-  p.tb = pl.tb;
-  if (cfg->dtype == WAN_BF16)
-    return vec ? launch_v<__nv_bfloat16, 4, kBwd>(p, pl, s) : launch_v<__nv_bfloat16, 1, kBwd>(p, pl, s);
-  return vec ? launch_v<float, 4, kBwd>(p, pl, s) : launch_v<float, 1, kBwd>(p, pl, s);
+int run_rope(const wan_dit_config* cfg, RopeParams& p, bool vec, bool dw, RopePlan& pl, cudaStream_t s) {
+  return cfg->dtype == WAN_BF16 ? run_typed<__nv_bfloat16, kBwd>(p, vec, dw, pl, s) : run_typed<float, kBwd>(p, vec, dw, pl, s);
 }
 
-// Quads divide the head: whole lanes of 8, and with split halves whole quads of each half.
-bool quads_fit(const wan_rope* r, const RopeParams& p) {
-  return p.d % 8 == 0 && (r->layout == WAN_ROPE_INTERLEAVED || p.pairs % 4 == 0);
+// Every lane has whole groups of 8 dims at one place of every head (the head divides 256 dims,
+// split halves are whole quads), and the block's sums fit into shared memory (sides of up to
+// 6144 dims; any for the forward).
+bool wide_fit(const wan_rope* r, const RopeParams& p, bool bwd) {
+  if (p.d < 8 || 256 % p.d != 0 || (r->layout == WAN_ROPE_HALF && p.pairs % 4 != 0)) return false;
+  return vec_smem(p, bwd) + 8 * 1024 <= 227 * 1024;
 }
 
 }  // namespace
@@ -497,11 +811,12 @@ int wan_qk_norm_rope_fwd(const wan_dit_config* cfg, const wan_rope* rope, const 
   p.d = cfg->head_dim, p.norm = norm, p.layout = rope->layout, p.n_axes = rope->n_axes;
   p.eps = cfg->eps, p.amplitude = static_cast<float>(rope->amplitude);
   fill_frequencies(rope, p);
-  const bool vec = quads_fit(rope, p) && rows_aligned(q, cfg->dtype) && rows_aligned(k, cfg->dtype) &&
+  const bool vec = wide_fit(rope, p, false) && rows_aligned(q, cfg->dtype) && rows_aligned(k, cfg->dtype) &&
                    rows_aligned(q_out, cfg->dtype) && rows_aligned(k_out, cfg->dtype);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   trace_launch_begin(WAN_KIND_NORM, s, 2.0 * rows * p.n * p.d * dtype_size(cfg->dtype));
-  const int st = run_rope<false>(cfg, p, vec, false, s);
+  RopePlan pl{};
+  const int st = run_rope<false>(cfg, p, vec, false, pl, s);
   trace_launch_end(WAN_KIND_NORM, s);
   return st;
 }
@@ -511,8 +826,9 @@ size_t wan_qk_norm_rope_workspace_bytes(const wan_dit_config* cfg, int rows, int
   size_t most = 0;
   for (int n : {cfg->heads, cfg->heads + kv_heads}) {
     if (n > kMaxHeads) continue;
-    const RopePlan pl = plan_rope(rows, n, true);
-    const size_t b = static_cast<size_t>(pl.blocks) * pl.tb * n * cfg->head_dim * 4;
+    const RopePlan any = plan_any(rows, n, true);
+    const int64_t vec = kDwBlocks + 1, other = static_cast<int64_t>(any.blocks) * any.tb;
+    const size_t b = static_cast<size_t>(vec > other ? vec : other) * n * cfg->head_dim * 4;
     most = b > most ? b : most;
   }
   return most;
@@ -570,17 +886,21 @@ int wan_qk_norm_rope_bwd(const wan_dit_config* cfg, const wan_rope* rope, const 
   p.d = cfg->head_dim, p.norm = norm, p.layout = rope->layout, p.n_axes = rope->n_axes;
   p.eps = cfg->eps, p.amplitude = static_cast<float>(rope->amplitude);
   fill_frequencies(rope, p);
-  const bool vec = quads_fit(rope, p) && rows_aligned(dq_out, cfg->dtype) && rows_aligned(dk_out, cfg->dtype) &&
+  const bool vec = wide_fit(rope, p, true) && rows_aligned(dq_out, cfg->dtype) && rows_aligned(dk_out, cfg->dtype) &&
                    rows_aligned(dq, cfg->dtype) && rows_aligned(dk, cfg->dtype) &&
                    (!normed || (rows_aligned(q, cfg->dtype) && rows_aligned(k, cfg->dtype)));
   trace_launch_begin(WAN_KIND_NORM, s, (normed ? 3.0 : 2.0) * rows * p.n * p.d * dtype_size(cfg->dtype));
-  int st = run_rope<true>(cfg, p, vec, normed, s);
+  RopePlan pl{};
+  int st = run_rope<true>(cfg, p, vec, normed, pl, s);
   if (st == WAN_OK && normed && (dw_q || dw_k)) {
-    const RopePlan pl = plan_rope(rows, p.n, true);
     const bool per_head = norm == WAN_QK_NORM_HEAD;
     const int most = per_head ? p.d : (p.H > p.n - p.H ? p.H : p.n - p.H) * p.d;
-    rope_dw_kernel<<<dim3((most + 31) / 32, with_k ? 2 : 1), dim3(32, 32), 0, s>>>(p.part, pl.blocks, pl.tb, p.n, p.H,
-                                                                                  p.d, per_head, dw_q, dw_k);
+    const int64_t wide = static_cast<int64_t>(p.n) * p.d, side_q = static_cast<int64_t>(p.H) * p.d;
+    const int part_rows = vec ? 0 : pl.blocks * pl.tb;
+    const DwSide dq_side{0, vec ? pl.q_blocks : part_rows, p.H, dw_q};
+    const DwSide dk_side{vec ? pl.q_blocks * side_q : side_q, vec ? pl.blocks - pl.q_blocks : part_rows, p.n - p.H, dw_k};
+    rope_dw_kernel<<<dim3((most + 31) / 32, with_k ? 2 : 1), dim3(32, 32), 0, s>>>(
+        p.part, dq_side, dk_side, vec ? side_q : wide, vec ? wide - side_q : wide, p.d, per_head);
     count_launches(1);
     st = check_launch();
   }
