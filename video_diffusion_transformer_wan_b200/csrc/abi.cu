@@ -70,6 +70,34 @@ int* device_error_flag() {
   return cache.get(&g_wan_error_flag, &p) == WAN_OK ? static_cast<int*>(p) : nullptr;
 }
 
+// ------------------------------------------------------------------ launch shapes
+int device_sms() {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    n = n > 0 ? n : 148;
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+int ResidentCache::get(const void* kernel, int threads, size_t smem, size_t max_smem) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::lock_guard<std::mutex> lk(mu_);
+  for (int i = 0; i < used_; ++i)
+    if (entry_[i].dev == dev && entry_[i].threads == threads && entry_[i].smem == smem) return entry_[i].blocks;
+  if (max_smem > 0) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(max_smem));
+  int per_sm = 0;
+  cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
+  const int blocks = device_sms() * (per_sm > 0 ? per_sm : 1);
+  entry_[used_ < kEntries ? used_++ : kEntries - 1] = {dev, threads, smem, blocks};
+  return blocks;
+}
+
 // ------------------------------------------------------------------ trace
 namespace {
 constexpr int kTracePairs = 16384;

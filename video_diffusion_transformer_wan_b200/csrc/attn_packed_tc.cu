@@ -770,10 +770,9 @@ int launch_attn_packed_tc(const PackedAttn& a, void* ws, size_t ws_bytes, cudaSt
   p.cap_in = a.cap > 0.f ? a.scale / a.cap : 0.f;
   p.prescale = a.slopes || p.mult < 0.f;
   p.err = device_error_flag();
-  int dev = 0, sms = 0;
+  int dev = 0;
   cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  p.ctas = sms > 0 && sms < kMaxCtas ? sms : kMaxCtas;
+  p.ctas = device_sms() < kMaxCtas ? device_sms() : kMaxCtas;
   const SplitLayout l = split_layout(a);
   p.slot_rows = l.slot_rows;
   if (ws) {

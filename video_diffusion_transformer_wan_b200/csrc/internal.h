@@ -62,6 +62,27 @@ inline int check_launch() {
   return e == cudaSuccess ? WAN_OK : WAN_ERR_CUDA;
 }
 
+// SMs of the current device, and blocks of a kernel that are resident on them at once; what
+// the runtime answers is kept per device (and per kernel and launch shape in ResidentCache,
+// one static object of each launcher).
+int device_sms();
+class ResidentCache {
+ public:
+  // `max_smem`: the dynamic shared memory that the kernel is allowed (0: as it is).
+  int get(const void* kernel, int threads, size_t smem, size_t max_smem = 0);
+
+ private:
+  struct Entry {
+    int dev, threads;
+    size_t smem;
+    int blocks;
+  };
+  static constexpr int kEntries = 16;
+  Entry entry_[kEntries] = {};
+  int used_ = 0;
+  std::mutex mu_;
+};
+
 // ---------------------------------------------------------------- tensor maps
 // 2D/3D bf16 tile maps with 128-byte swizzle. dims/strides innermost first; strides
 // in bytes for dims >= 1. Returns false if the driver rejects the map.

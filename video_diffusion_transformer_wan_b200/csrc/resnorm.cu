@@ -22,6 +22,7 @@
 #include "checks.h"
 #include "internal.h"
 #include "packed.cuh"
+#include "ptx.cuh"
 
 namespace wan {
 namespace {
@@ -231,11 +232,50 @@ __device__ __forceinline__ void join_warps(float4 s, float2 g, int kind, float i
   const float m2 = warp_sum(fmaf(s.x * off, off, s.z));
   r = rsqrtf(fmaf(m2, inv_d, eps));
   a = warp_sum(fmaf(g.y, off, g.x));
-  b = warp_sum(g.y);
+  b = kind == WAN_NORM_LAYER ? warp_sum(g.y) : 0.f;
 }
 
-template <typename T, int NU, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads) gated_residual_norm_bwd_kernel(const ResNormParams p) {
+using F2 = unsigned long long;  // two fp32
+__device__ __forceinline__ float sum_of(F2 v) {
+  const float2 f = f2_unpack(v);
+  return f.x + f.y;
+}
+__device__ __forceinline__ void unpack4(const Raw8<__nv_bfloat16>& r, F2 (&v)[4]) {
+  v[0] = f2_pack(bf16_lo(r.u.x), bf16_hi(r.u.x)), v[1] = f2_pack(bf16_lo(r.u.y), bf16_hi(r.u.y));
+  v[2] = f2_pack(bf16_lo(r.u.z), bf16_hi(r.u.z)), v[3] = f2_pack(bf16_lo(r.u.w), bf16_hi(r.u.w));
+}
+__device__ __forceinline__ void unpack4(const Raw8<float>& r, F2 (&v)[4]) {
+  v[0] = f2_pack(r.a.x, r.a.y), v[1] = f2_pack(r.a.z, r.a.w), v[2] = f2_pack(r.b.x, r.b.y), v[3] = f2_pack(r.b.z, r.b.w);
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* at, const F2 (&v)[4]) {
+  float f[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 x = f2_unpack(v[k]);
+    f[2 * k] = x.x, f[2 * k + 1] = x.y;
+  }
+  store_vec8(at, f);
+}
+
+// A thread's 8 columns of `units` vectors in shared memory, 16 bytes apart by thread: no
+// conflicts, no exchange.
+__device__ __forceinline__ void sm_get(const float4* sm, int which, F2 (&v)[4]) {
+  const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(sm + (2 * which) * blockDim.x + threadIdx.x);
+  const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(sm + (2 * which + 1) * blockDim.x + threadIdx.x);
+  v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+}
+__device__ __forceinline__ void sm_put(float4* sm, int which, const F2 (&v)[4]) {
+  *reinterpret_cast<ulonglong2*>(sm + (2 * which) * blockDim.x + threadIdx.x) = make_ulonglong2(v[0], v[1]);
+  *reinterpret_cast<ulonglong2*>(sm + (2 * which + 1) * blockDim.x + threadIdx.x) = make_ulonglong2(v[2], v[3]);
+}
+size_t bwd_smem(int threads, int nu) { return static_cast<size_t>(threads) * nu * 5 * 32; }
+
+// The document's vectors (gate w_post, w (1 + scale)) and the three column sums live in shared
+// memory: in registers they left room for one block an SM, or spilled.
+template <typename T, int NU, int kMaxThreads, int kMinBlocks>
+__global__ void __launch_bounds__(kMaxThreads, kMinBlocks) gated_residual_norm_bwd_kernel(const ResNormParams p) {
+  extern __shared__ float4 vec[];  // per unit: g, sc, s0, s1, s2
   __shared__ RowSums sm;
   const int tpr = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int col[NU];
@@ -253,165 +293,191 @@ __global__ void __launch_bounds__(kMaxThreads) gated_residual_norm_bwd_kernel(co
     sm.x[0][i] = sm.y[0][i] = make_float4(0.f, 0.f, 0.f, 0.f);
     sm.xg[0][i] = sm.k[0][i] = make_float2(0.f, 0.f);
   }
+  const F2 zero[4] = {};
+#pragma unroll
+  for (int u = 0; u < NU; ++u)
+#pragma unroll
+    for (int k = 0; k < 5; ++k) sm_put(vec, 5 * u + k, zero);
   __syncthreads();
   const RowSpan span = block_rows(p, blockIdx.x, gridDim.x);
   if (span.lo >= span.hi) return;
-  float g[NU][8], sc[NU][8];                      // gate w_post; w (1 + scale)
-  float s0[NU][8] = {}, s1[NU][8] = {}, s2[NU][8] = {};
   int doc = -1, half = 0;
   int64_t doc_end = -1;
   auto flush = [&]() {
     if (!p.part) return;
     float* out = p.part + (static_cast<int64_t>(blockIdx.x) + doc) * 3 * p.D;
 #pragma unroll
-    for (int u = 0; u < NU; ++u) {
-      if (on[u]) {
-        store_vec8(out + col[u], s0[u]);
-        store_vec8(out + p.D + col[u], s1[u]);
-        store_vec8(out + 2 * static_cast<int64_t>(p.D) + col[u], s2[u]);
-      }
+    for (int u = 0; u < NU; ++u)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s0[u][i] = s1[u][i] = s2[u][i] = 0.f;
-    }
+      for (int k = 0; k < 3; ++k) {
+        F2 v[4];
+        sm_get(vec, 5 * u + 2 + k, v);
+        if (on[u]) store4(out + static_cast<int64_t>(k) * p.D + col[u], v);
+        sm_put(vec, 5 * u + 2 + k, zero);
+      }
   };
-  for (int64_t row = span.lo; row < span.hi; ++row, half ^= 1) {
-    float x[NU][8], y[NU][8], dh[NU][8];
-    Raw8<float> rg[NU];
-    {
-      Raw8<float> rx[NU];
-      Raw8<T> ry[NU], rh[NU];
+  const float *xp = p.x + span.lo * p.D, *up = p.dx_out + (p.dx_out ? span.lo * p.D : 0);
+  const T *hp = static_cast<const T*>(p.dh) + span.lo * p.D, *yp = static_cast<const T*>(p.y) + span.lo * p.D;
+  float* dxp = p.dx + span.lo * p.D;
+  T* dyp = static_cast<T*>(p.dy) + span.lo * p.D;
+  for (int64_t row = span.lo; row < span.hi;
+       ++row, half ^= 1, xp += p.D, hp += p.D, yp += p.D, dxp += p.D, dyp += p.D, up += p.dx_out ? p.D : 0) {
+    Raw8<float> rx[NU], rg[NU];
+    Raw8<T> ry[NU], rh[NU];
+    const bool more = row + 1 < span.hi;
 #pragma unroll
-      for (int u = 0; u < NU; ++u)
-        if (on[u]) {
-          load_raw8(rx[u], p.x + row * p.D + col[u]);
-          load_raw8(rh[u], static_cast<const T*>(p.dh) + row * p.D + col[u]);
-          load_raw8(ry[u], static_cast<const T*>(p.y) + row * p.D + col[u]);
-          if (p.dx_out) load_raw8(rg[u], p.dx_out + row * p.D + col[u]);
-          if (row + 1 < span.hi) {  // the next row on its way into L2
-            ask_l2(p.x + (row + 1) * p.D + col[u]);
-            ask_l2(static_cast<const T*>(p.dh) + (row + 1) * p.D + col[u]);
-            ask_l2(static_cast<const T*>(p.y) + (row + 1) * p.D + col[u]);
-            if (p.dx_out) ask_l2(p.dx_out + (row + 1) * p.D + col[u]);
-          }
-        }
-      if (row >= doc_end) {
-        if (doc >= 0) flush();
-        doc = doc_of_row(p.cu, p.n_docs, static_cast<int>(row));
-        doc_end = max(__ldg(p.cu + doc + 1), static_cast<int>(row) + 1);
-#pragma unroll
-        for (int u = 0; u < NU; ++u)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int c = col[u] + i;
-            if (!on[u]) continue;
-            g[u][i] = at<T>(p.w_post, c, 1.f) * (p.gate >= 0 ? mod_at(p, doc, p.gate, c) : 1.f);
-            sc[u][i] = at<T>(p.w_pre, c, 1.f) * (p.chunk >= 0 ? 1.f + mod_at(p, doc, 3 * p.chunk + 1, c) : 1.f);
-          }
+    for (int u = 0; u < NU; ++u) {
+      rx[u] = Raw8<float>{}, rg[u] = Raw8<float>{}, ry[u] = Raw8<T>{}, rh[u] = Raw8<T>{};
+      if (!on[u]) continue;
+      load_raw8(rx[u], xp + col[u]);
+      load_raw8(rh[u], hp + col[u]);
+      load_raw8(ry[u], yp + col[u]);
+      if (more) {  // the next row on its way into L2
+        ask_l2(xp + p.D + col[u]);
+        ask_l2(hp + p.D + col[u]);
+        ask_l2(yp + p.D + col[u]);
+        if (p.dx_out) ask_l2(up + p.D + col[u]);
       }
+    }
+    if (row >= doc_end) {
+      if (doc >= 0) flush();
+      doc = doc_of_row(p.cu, p.n_docs, static_cast<int>(row));
+      doc_end = max(__ldg(p.cu + doc + 1), static_cast<int>(row) + 1);
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
-        if (on[u]) {
-          unpack8(rx[u], x[u]);
-          unpack8(rh[u], dh[u]);
-          unpack8(ry[u], y[u]);
-          if (!p.dx_out) rg[u] = Raw8<float>{};
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[u][i] = dh[u][i] = y[u][i] = g[u][i] = sc[u][i] = 0.f;
-          rg[u] = Raw8<float>{};
-        }
-      }
-    }
-    // This warp's sums: of x about its own mean, with dn = dh sc, and of y.
-    float sum = 0.f, own = 0.f, m2 = 0.f, ga = 0.f, gb = 0.f;
-    if (p.pre == WAN_NORM_LAYER) {
-#pragma unroll
-      for (int u = 0; u < NU; ++u)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum += x[u][i];
-      sum = warp_sum(sum);
-      own = sum * inv_cols;
-    }
-#pragma unroll
-    for (int u = 0; u < NU; ++u)
-      if (on[u])
+        if (!on[u]) continue;
+        float g[8], sc[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float v = x[u][i] - own, dn = dh[u][i] * sc[u][i];
-          m2 = fmaf(v, v, m2);
-          ga = fmaf(dn, v, ga);
-          gb += dn;
+          const int c = col[u] + i;
+          g[i] = at<T>(p.w_post, c, 1.f) * (p.gate >= 0 ? mod_at(p, doc, p.gate, c) : 1.f);
+          sc[i] = at<T>(p.w_pre, c, 1.f) * (p.chunk >= 0 ? 1.f + mod_at(p, doc, 3 * p.chunk + 1, c) : 1.f);
         }
-    m2 = warp_sum(m2), ga = warp_sum(ga), gb = warp_sum(gb);
-    float ysum = 0.f, yown = 0.f, ym2 = 0.f;
-    if (p.post != WAN_NORM_NONE) {
-      if (p.post == WAN_NORM_LAYER) {
-#pragma unroll
-        for (int u = 0; u < NU; ++u)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) ysum += y[u][i];
-        ysum = warp_sum(ysum);
-        yown = ysum * inv_cols;
+        const F2 g4[4] = {f2_pack(g[0], g[1]), f2_pack(g[2], g[3]), f2_pack(g[4], g[5]), f2_pack(g[6], g[7])};
+        const F2 s4[4] = {f2_pack(sc[0], sc[1]), f2_pack(sc[2], sc[3]), f2_pack(sc[4], sc[5]), f2_pack(sc[6], sc[7])};
+        sm_put(vec, 5 * u, g4);
+        sm_put(vec, 5 * u + 1, s4);
       }
+    }
+    // This warp's sums: of x about its own mean, with dn = dh sc, and of y. Columns that are
+    // not there hold zeros and add their own mean's squares: they are left out.
+    float own = 0.f, sum = 0.f, yown = 0.f, ysum = 0.f;
+    if (p.pre == WAN_NORM_LAYER || p.post == WAN_NORM_LAYER) {
+      F2 a = 0ull, b = 0ull;
+#pragma unroll
+      for (int u = 0; u < NU; ++u) {
+        F2 x[4], y[4];
+        unpack4(rx[u], x);
+        unpack4(ry[u], y);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) a = f2_add(a, x[k]), b = f2_add(b, y[k]);
+      }
+      if (p.pre == WAN_NORM_LAYER) sum = warp_sum(sum_of(a)), own = sum * inv_cols;
+      if (p.post == WAN_NORM_LAYER) ysum = warp_sum(sum_of(b)), yown = ysum * inv_cols;
+    }
+    {
+      F2 m2 = 0ull, ga = 0ull, gb = 0ull, ym2 = 0ull;
+      const F2 own2 = f2_splat(-own), yown2 = f2_splat(-yown);
 #pragma unroll
       for (int u = 0; u < NU; ++u)
-        if (on[u])
+        if (on[u]) {
+          F2 x[4], y[4], h[4], sc[4];
+          unpack4(rx[u], x);
+          unpack4(rh[u], h);
+          sm_get(vec, 5 * u + 1, sc);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) ym2 = fmaf(y[u][i] - yown, y[u][i] - yown, ym2);
-      ym2 = warp_sum(ym2);
+          for (int k = 0; k < 4; ++k) {
+            const F2 v = f2_add(x[k], own2), dn = f2_mul(h[k], sc[k]);
+            m2 = f2_fma(v, v, m2);
+            ga = f2_fma(dn, v, ga);
+            gb = f2_add(gb, dn);
+          }
+          if (p.post != WAN_NORM_NONE) {
+            unpack4(ry[u], y);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const F2 v = f2_add(y[k], yown2);
+              ym2 = f2_fma(v, v, ym2);
+            }
+          }
+        }
+      const float m = warp_sum(sum_of(m2)), a = warp_sum(sum_of(ga));
+      const float c = p.pre == WAN_NORM_LAYER ? warp_sum(sum_of(gb)) : 0.f;
+      const float ym = p.post != WAN_NORM_NONE ? warp_sum(sum_of(ym2)) : 0.f;
+      if (lane == 0) {
+        sm.x[half][warp] = make_float4(warp_cols, sum, m, 0.f);
+        sm.xg[half][warp] = make_float2(a, c);
+        sm.y[half][warp] = make_float4(warp_cols, ysum, ym, 0.f);
+      }
     }
-    if (lane == 0) {
-      sm.x[half][warp] = make_float4(warp_cols, sum, m2, 0.f);
-      sm.xg[half][warp] = make_float2(ga, gb);
-      sm.y[half][warp] = make_float4(warp_cols, ysum, ym2, 0.f);
-    }
+    // Read as late as the barrier still hides it: held from the start it cost the second block.
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+      if (on[u] && p.dx_out) load_raw8(rg[u], up + col[u]);
     __syncthreads();
     float mean, r, a, c;
     join_warps(sm.x[half][lane], sm.xg[half][lane], p.pre, inv_d, p.eps, mean, r, a, c);
     // dn n sums to a r; G = dx_out + r (dn - [mean dn] - n mean(dn n))
     a *= r * r * inv_d;
-    c = p.pre == WAN_NORM_LAYER ? c * inv_d : 0.f;
-    float ymean = 0.f, ry = 1.f;
+    c *= inv_d;
+    float ymean = 0.f, ry_ = 1.f;
     if (p.post != WAN_NORM_NONE) {
       float d0, d1;
-      join_warps(sm.y[half][lane], make_float2(0.f, 0.f), p.post, inv_d, p.eps, ymean, ry, d0, d1);
+      join_warps(sm.y[half][lane], make_float2(0.f, 0.f), p.post, inv_d, p.eps, ymean, ry_, d0, d1);
     }
-    float k0 = 0.f, k1 = 0.f;
+    F2 yn[NU][4], gg[NU][4], k0 = 0ull, k1 = 0ull;
+    const F2 mean2 = f2_splat(-mean), r2 = f2_splat(r), a2 = f2_splat(-a), c2 = f2_splat(-c), ymean2 = f2_splat(-ymean),
+             ry2 = f2_splat(ry_), scale2 = f2_splat(p.residual_scale);
 #pragma unroll
     for (int u = 0; u < NU; ++u)
       if (on[u]) {
-        float gv[8], dx[8];
-        unpack8(rg[u], gv);
+        F2 x[4], h[4], sc[4], s0[4], s1[4], s2[4], g[4], dx[4], gv[4];
+        unpack4(rx[u], x);
+        unpack4(rh[u], h);
+        unpack4(ry[u], yn[u]);
+        unpack4(rg[u], gv);
+        sm_get(vec, 5 * u + 1, sc);
+        sm_get(vec, 5 * u + 2, s0);
+        sm_get(vec, 5 * u + 3, s1);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float v = x[u][i] - mean;
-          s0[u][i] += dh[u][i];
-          s1[u][i] = fmaf(dh[u][i], v * r, s1[u][i]);
-          const float G = fmaf(r, fmaf(dh[u][i], sc[u][i], -c) - v * a, gv[i]);
-          dx[i] = p.residual_scale * G;
-          y[u][i] = (y[u][i] - ymean) * ry;
-          s2[u][i] = fmaf(G, y[u][i], s2[u][i]);
-          x[u][i] = G * g[u][i];
-          k0 = fmaf(x[u][i], y[u][i], k0);
-          k1 += x[u][i];
+        for (int k = 0; k < 4; ++k) {
+          const F2 v = f2_add(x[k], mean2);
+          s0[k] = f2_add(s0[k], h[k]);
+          s1[k] = f2_fma(h[k], f2_mul(v, r2), s1[k]);
+          gv[k] = f2_fma(r2, f2_fma(v, a2, f2_fma(h[k], sc[k], c2)), gv[k]);
+          dx[k] = f2_mul(scale2, gv[k]);
         }
-        store_vec8(p.dx + row * p.D + col[u], dx);
+        sm_put(vec, 5 * u + 2, s0);
+        sm_put(vec, 5 * u + 3, s1);
+        store4(dxp + col[u], dx);
+        sm_get(vec, 5 * u + 4, s2);
+        sm_get(vec, 5 * u, g);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          yn[u][k] = f2_mul(f2_add(yn[u][k], ymean2), ry2);
+          s2[k] = f2_fma(gv[k], yn[u][k], s2[k]);
+          gg[u][k] = f2_mul(gv[k], g[k]);
+          k0 = f2_fma(gg[u][k], yn[u][k], k0);
+          k1 = f2_add(k1, gg[u][k]);
+        }
+        sm_put(vec, 5 * u + 4, s2);
       }
     float ka = 0.f, kc = 0.f;
     if (p.post != WAN_NORM_NONE) {
-      k0 = warp_sum(k0), k1 = warp_sum(k1);
-      if (lane == 0) sm.k[half][warp] = make_float2(k0, k1);
+      const float x0 = warp_sum(sum_of(k0)), x1 = p.post == WAN_NORM_LAYER ? warp_sum(sum_of(k1)) : 0.f;
+      if (lane == 0) sm.k[half][warp] = make_float2(x0, x1);
       __syncthreads();
       const float2 k = sm.k[half][lane];
       ka = warp_sum(k.x) * inv_d;
-      kc = p.post == WAN_NORM_LAYER ? warp_sum(k.y) * inv_d : 0.f;
+      if (p.post == WAN_NORM_LAYER) kc = warp_sum(k.y) * inv_d;
     }
+    const F2 ka2 = f2_splat(-ka), kc2 = f2_splat(-kc);
 #pragma unroll
     for (int u = 0; u < NU; ++u)
       if (on[u]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[u][i] = ry * (x[u][i] - kc - y[u][i] * ka);
-        store_vec8(static_cast<T*>(p.dy) + row * p.D + col[u], y[u]);
+        for (int k = 0; k < 4; ++k) gg[u][k] = f2_mul(ry2, f2_fma(yn[u][k], ka2, f2_add(gg[u][k], kc2)));
+        store4(dyp + col[u], gg[u]);
       }
   }
   flush();
@@ -501,22 +567,17 @@ __global__ void __launch_bounds__(128) resnorm_weight_sums_kernel(const ResNormP
 int block_threads(int D, int nu) { return (D / 8 + nu * 32 - 1) / (nu * 32) * 32; }
 
 // Blocks of one launch: every resident slot of the card, no more than rows.
-template <typename K>
-int resident_blocks(K kernel, int threads, int rows) {
-  int dev = 0, sms = 0, per_sm = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0);
-  int64_t n = static_cast<int64_t>(sms > 0 ? sms : 148) * (per_sm > 0 ? per_sm : 1);
-  n = n < kMaxBlocks ? n : kMaxBlocks;
-  return static_cast<int>(n < rows ? n : (rows > 0 ? rows : 1));
+int blocks_of(int resident, int rows) {
+  const int n = resident < kMaxBlocks ? resident : kMaxBlocks;
+  return n < rows ? n : (rows > 0 ? rows : 1);
 }
 
 template <typename T, int NU, int kMaxThreads>
 int launch_fwd(const ResNormParams& p, cudaStream_t s) {
+  static ResidentCache resident;
   const int th = block_threads(p.D, NU);
   auto kernel = gated_residual_norm_kernel<T, NU, kMaxThreads>;
-  kernel<<<resident_blocks(kernel, th, p.rows), th, 0, s>>>(p);
+  kernel<<<blocks_of(resident.get(reinterpret_cast<const void*>(kernel), th, 0), p.rows), th, 0, s>>>(p);
   return check_launch();
 }
 template <typename T>
@@ -525,20 +586,22 @@ int run_fwd(const ResNormParams& p, cudaStream_t s) {
   return launch_fwd<T, 2, 512>(p, s);
 }
 
-template <typename T, int NU, int kMaxThreads>
+template <typename T, int NU, int kMaxThreads, int kMinBlocks>
 int launch_bwd(const ResNormParams& p, cudaStream_t s, int* blocks) {
   const int th = block_threads(p.D, NU);
-  auto kernel = gated_residual_norm_bwd_kernel<T, NU, kMaxThreads>;
-  *blocks = resident_blocks(kernel, th, p.rows);
-  kernel<<<*blocks, th, 0, s>>>(p);
+  auto kernel = gated_residual_norm_bwd_kernel<T, NU, kMaxThreads, kMinBlocks>;
+  const size_t smem = bwd_smem(th, NU);
+  static ResidentCache resident;
+  *blocks = blocks_of(resident.get(reinterpret_cast<const void*>(kernel), th, smem, bwd_smem(kMaxThreads, NU)), p.rows);
+  kernel<<<*blocks, th, smem, s>>>(p);
   return check_launch();
 }
 template <typename T>
 int run_bwd(const ResNormParams& p, const wan_residual_norm_grads& g, float* total, cudaStream_t s) {
   int blocks = 0, st = WAN_OK;
   if (p.n_docs > 0)
-    st = p.D <= 2048 ? launch_bwd<T, 1, 256>(p, s, &blocks)
-                     : p.D <= 5120 ? launch_bwd<T, 1, 640>(p, s, &blocks) : launch_bwd<T, 2, 512>(p, s, &blocks);
+    st = p.D <= 2048 ? launch_bwd<T, 1, 256, 3>(p, s, &blocks)
+                     : p.D <= 5120 ? launch_bwd<T, 2, 320, 2>(p, s, &blocks) : launch_bwd<T, 2, 512, 1>(p, s, &blocks);
   if (st != WAN_OK || !p.part) return st;
   if (p.n_docs > 0) {
     const int docs_y = p.n_docs < 1024 ? p.n_docs : 1024;

@@ -661,7 +661,8 @@ int run_any(const RopeParams& p, const RopePlan& pl, cudaStream_t s) {
   return WAN_ERR_UNSUPPORTED;
 }
 
-// Dynamic shared memory of one block (see the kernel).
+// Dynamic shared memory of one block (see the kernel), and the most that its own leaves of 227 KB.
+constexpr size_t kMostSmem = 220 * 1024;
 size_t vec_smem(const RopeParams& p, bool bwd) {
   if (p.norm == WAN_QK_NORM_NONE) return 0;
   const size_t widest = static_cast<size_t>(p.H > p.n - p.H ? p.H : p.n - p.H) * p.d;
@@ -674,12 +675,8 @@ template <typename T, int CH, bool kHalf, bool kBwd>
 int launch_vec(const RopeParams& p, RopePlan& pl, bool dw, cudaStream_t s) {
   auto kernel = qk_norm_rope_kernel<T, CH, kHalf, kBwd>;
   const size_t smem = vec_smem(p, kBwd);
-  int dev = 0, sms = 0, per_sm = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (smem > 40 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kWarps * 32, smem);
-  int most = (sms > 0 ? sms : 148) * (per_sm > 0 ? per_sm : 1);
+  static ResidentCache resident;
+  int most = resident.get(reinterpret_cast<const void*>(kernel), kWarps * 32, smem, kMostSmem);
   if (dw && most > kDwBlocks) most = kDwBlocks;
   const int need = (p.rows + kWarps - 1) / kWarps;  // of each side
   pl.q_blocks = static_cast<int>(static_cast<int64_t>(most) * p.H / p.n);
@@ -773,7 +770,7 @@ int run_rope(const wan_dit_config* cfg, RopeParams& p, bool vec, bool dw, RopePl
 // 6144 dims; any for the forward).
 bool wide_fit(const wan_rope* r, const RopeParams& p, bool bwd) {
   if (p.d < 8 || 256 % p.d != 0 || (r->layout == WAN_ROPE_HALF && p.pairs % 4 != 0)) return false;
-  return vec_smem(p, bwd) + 8 * 1024 <= 227 * 1024;
+  return vec_smem(p, bwd) <= kMostSmem;
 }
 
 }  // namespace

@@ -12,7 +12,7 @@ from __future__ import annotations
 import ctypes
 from typing import Optional, Sequence
 
-from . import Config, WAN_BF16, _check, _lib, _stream
+from . import Config, WAN_BF16, _check, _lib
 
 __all__ = [
     "RopeSpec", "ResidualNormSpec", "Documents", "rope", "residual_norm", "documents", "qk_norm_rope_fwd",
@@ -75,9 +75,23 @@ def signatures():
 
 
 # ------------------------------------------------------------------ argument checks
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
+
+
+def _stream(stream):
+    """The stream given, or the current one of the current device."""
+    if stream is not None:
+        return stream if isinstance(stream, int) else stream.cuda_stream
+    torch = _torch()
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _act(cfg):
@@ -86,20 +100,22 @@ def _act(cfg):
 
 class _Args:
     """Collects the tensors of one call: their device must be one CUDA device."""
+    __slots__ = ("where", "device")
 
     def __init__(self, where):
-        self.where, self.device = where, None
+        self.where, self.device = where, -1
 
     def fail(self, what):
         raise ValueError(f"{self.where}: {what}")
 
     def _seen(self, t, name):
-        if not t.is_cuda:
-            self.fail(f"{name} is not on a CUDA device")
-        if self.device is None:
-            self.device = t.device
-        elif self.device != t.device:
-            self.fail(f"{name} is on {t.device}, the other tensors on {self.device}")
+        d = t.get_device()  # -1 on the CPU
+        if d != self.device or d < 0:
+            if d < 0:
+                self.fail(f"{name} is not on a CUDA device")
+            if self.device >= 0:
+                self.fail(f"{name} is on device {d}, the other tensors on {self.device}")
+            self.device = d
 
     def array(self, t, name, dtype, shape, optional=False):
         """Pointer of a contiguous tensor of this type and shape."""
@@ -108,7 +124,7 @@ class _Args:
                 self.fail(f"{name} is required")
             return None
         self._seen(t, name)
-        if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
             self.fail(f"{name} must be contiguous {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)} "
                       f"strides {t.stride()}")
         return t.data_ptr()
@@ -120,7 +136,7 @@ class _Args:
                 self.fail(f"{name} is required")
             return None
         self._seen(t, name)
-        if t.dtype != dtype or t.dim() != 2 or tuple(t.shape) != (n, width) or (width > 1 and t.stride(1) != 1):
+        if t.dtype != dtype or t.shape != (n, width) or (width > 1 and t.stride(1) != 1):
             self.fail(f"{name} must be {dtype} [{n}, {width}] with dense rows, got {t.dtype} {tuple(t.shape)} strides "
                       f"{t.stride()}")
         stride = t.stride(0) if n > 1 else width  # the stride of a single row says nothing
@@ -135,12 +151,12 @@ class _Args:
         return ws.data_ptr(), ws.numel() * ws.element_size()
 
     def call(self, fn, stream, *args):
-        torch = _torch()
-        if self.device is None or self.device.index == torch.cuda.current_device():
-            _check(getattr(_lib(), fn)(*args, _stream(stream)), fn)
+        cuda, f = _torch().cuda, getattr(_lib(), fn)
+        if self.device == cuda.current_device():
+            _check(f(*args, _stream(stream)), fn)
             return
-        with torch.cuda.device(self.device):
-            _check(getattr(_lib(), fn)(*args, _stream(stream)), fn)
+        with cuda.device(self.device):
+            _check(f(*args, _stream(stream)), fn)
 
 
 def _choice(table, value, name):
