@@ -1,12 +1,15 @@
-// Attention inside packed documents on the CUDA cores, with full fp32 arithmetic, and its
-// gradient: one pass over the keys with a running maximum and sum; the gradient recomputes
-// the probabilities from the stored log-sums, p = e^(s - lse), ds = p (dp - delta) with
-// delta = sum(do * o), in one kernel per side (dq over the keys, dk and dv over the
-// queries), so that nothing is added across blocks.
+// Attention inside packed documents in fp32 on the CUDA cores, and its gradient: one pass
+// over the keys with a running maximum and sum; the gradient recomputes the probabilities
+// from the stored log-sums, p = e^(s - lse), ds = p (dp - delta) (1 - tanh^2) with
+// delta = sum(do * o), in one kernel per side (dq over the keys, dk and dv over the queries),
+// so that nothing is added across blocks.
 //
-// A block takes 32 rows of one document and head; eight lanes hold a row (a quarter of a
-// 32-wide tile of scores and an eighth of the head each), so row maxima and sums stay
-// inside a warp. Bound by shared-memory reads (two per multiply-add).
+// A block of 128 threads owns 16 rows (queries, or keys) of one document and head and walks
+// tiles of 32 rows of the other side, double-buffered by cp.async. 16 threads share two rows:
+// in a score product each has 2 x 2 entries, 16 multiply-adds per four 16-byte shared loads;
+// in a product with the tile's values 2 rows x 4 (or 2 x 4) dims. Row maxima and sums are
+// shuffles over the 16. fp32 models are small: few rows and long latencies bound this, hence
+// tiles of 16 rows (346 rows of 2 heads are 48 blocks).
 #include <math.h>
 
 #include "internal.h"
@@ -15,9 +18,10 @@
 namespace wan {
 namespace {
 
-constexpr int kR = 32;         // rows and columns of a tile
-constexpr int kThreads = 256;  // eight lanes a row
-constexpr int kMaxD = 128;
+constexpr int kR = 16;         // rows of a block
+constexpr int kC = 32;         // rows of a tile of the other side
+constexpr int kThreads = 128;
+constexpr int kSp = kC + 4;    // pitch of a tile of probabilities
 
 struct Doc {
   int q0, Lq, k0, Lk, off, prefix;
@@ -40,29 +44,80 @@ __device__ __forceinline__ bool block_tile(const int32_t* cu, int n_docs, int ro
   return found[0] != 0;
 }
 
-template <typename T>
-__device__ __forceinline__ void load_tile(float* dst, const void* src, int64_t stride, int64_t row0, int valid, int col0,
-                                          int d) {
-  for (int i = threadIdx.x; i < kR * d; i += kThreads) {
-    const int r = i / d, c = i - r * d;
-    dst[r * (d + 1) + c] = r < valid ? to_f32<T>(static_cast<const T*>(src)[(row0 + r) * stride + col0 + c]) : 0.f;
+// Rows [row0, row0 + n) of a matrix into shared memory (pitch D + 4), rows from `valid` on and
+// dims from d on as zeros.
+template <int D>
+__device__ __forceinline__ void load_async(float* dst, const void* src, int64_t stride, int64_t row0, int n, int valid,
+                                           int col0, int d) {
+  for (int i = threadIdx.x; i < n * (D / 4); i += kThreads) {
+    const int r = i / (D / 4), c = i - r * (D / 4);
+    const bool there = r < valid && 4 * c < d;
+    const float* from = static_cast<const float*>(src) + (there ? (row0 + r) * stride + col0 + 4 * c : 0);
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst + r * (D + 4) + 4 * c));
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
   }
 }
+__device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void async_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
-__device__ __forceinline__ float sum8(float v) {
+// s[i][j] = row (2 ty + i) of a . row (tx + 16 j) of b.
+template <int D>
+__device__ __forceinline__ void dot_2x2(const float* a, const float* b, float (&s)[2][2]) {
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  const float4 *a0 = reinterpret_cast<const float4*>(a + (2 * ty) * (D + 4)), *a1 = reinterpret_cast<const float4*>(a + (2 * ty + 1) * (D + 4));
+  const float4 *b0 = reinterpret_cast<const float4*>(b + tx * (D + 4)), *b1 = reinterpret_cast<const float4*>(b + (tx + 16) * (D + 4));
+  s[0][0] = s[0][1] = s[1][0] = s[1][1] = 0.f;
+#pragma unroll 8
+  for (int c = 0; c < D / 4; ++c) {
+    const float4 x0 = a0[c], x1 = a1[c], y0 = b0[c], y1 = b1[c];
+    s[0][0] = fmaf(x0.w, y0.w, fmaf(x0.z, y0.z, fmaf(x0.y, y0.y, fmaf(x0.x, y0.x, s[0][0]))));
+    s[0][1] = fmaf(x0.w, y1.w, fmaf(x0.z, y1.z, fmaf(x0.y, y1.y, fmaf(x0.x, y1.x, s[0][1]))));
+    s[1][0] = fmaf(x1.w, y0.w, fmaf(x1.z, y0.z, fmaf(x1.y, y0.y, fmaf(x1.x, y0.x, s[1][0]))));
+    s[1][1] = fmaf(x1.w, y1.w, fmaf(x1.z, y1.z, fmaf(x1.y, y1.y, fmaf(x1.x, y1.x, s[1][1]))));
+  }
+}
+// o[i] += row (2 ty + i) of p (32 entries) times b, dims 4 tx + 64 k.
+template <int D>
+__device__ __forceinline__ void add_product(const float* p, const float* b, float4 (&o)[2][D / 64]) {
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+#pragma unroll 2
+  for (int j = 0; j < kC; j += 4) {
+    const float4 p0 = *reinterpret_cast<const float4*>(p + (2 * ty) * kSp + j), p1 = *reinterpret_cast<const float4*>(p + (2 * ty + 1) * kSp + j);
+    const float w0[4] = {p0.x, p0.y, p0.z, p0.w}, w1[4] = {p1.x, p1.y, p1.z, p1.w};
 #pragma unroll
-  for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o, 8);
+    for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+      for (int k = 0; k < D / 64; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(b + (j + jj) * (D + 4) + 4 * tx + 64 * k);
+        o[0][k].x = fmaf(w0[jj], v.x, o[0][k].x), o[0][k].y = fmaf(w0[jj], v.y, o[0][k].y);
+        o[0][k].z = fmaf(w0[jj], v.z, o[0][k].z), o[0][k].w = fmaf(w0[jj], v.w, o[0][k].w);
+        o[1][k].x = fmaf(w1[jj], v.x, o[1][k].x), o[1][k].y = fmaf(w1[jj], v.y, o[1][k].y);
+        o[1][k].z = fmaf(w1[jj], v.z, o[1][k].z), o[1][k].w = fmaf(w1[jj], v.w, o[1][k].w);
+      }
+  }
+}
+template <int D>
+__device__ __forceinline__ void store_rows(void* base, int64_t stride, int64_t row0, int valid, int col0, int d,
+                                           const float4 (&o)[2][D / 64], const float (&f)[2]) {
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k)
+      if (2 * ty + i < valid && 4 * tx + 64 * k < d)
+        *reinterpret_cast<float4*>(static_cast<float*>(base) + (row0 + 2 * ty + i) * stride + col0 + 4 * tx + 64 * k) =
+            make_float4(o[i][k].x * f[i], o[i][k].y * f[i], o[i][k].z * f[i], o[i][k].w * f[i]);
+}
+
+__device__ __forceinline__ float sum16(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o, 16);
   return v;
 }
-__device__ __forceinline__ float max8(float v) {
+__device__ __forceinline__ float max16(float v) {
 #pragma unroll
-  for (int o = 4; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o, 8));
+  for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o, 16));
   return v;
-}
-__device__ __forceinline__ float dot_rows(const float* a, const float* b, int d) {
-  float s = 0.f;
-  for (int c = 0; c < d; ++c) s = fmaf(a[c], b[c], s);
-  return s;
 }
 // Score of query position `pos` (i + off) and key j from q.k; d s / d(q.k) / scale in `turn`.
 __device__ __forceinline__ float score(float dot, const PackedAttn& p, float slope, int pos, int j, float& turn) {
@@ -76,254 +131,297 @@ __device__ __forceinline__ float score(float dot, const PackedAttn& p, float slo
   return s - slope * fabsf(static_cast<float>(pos - j));
 }
 
-template <typename T>
+template <int D>
 __global__ void __launch_bounds__(kThreads) packed_fwd_kernel(const PackedAttn p) {
-  extern __shared__ float sm[];
-  const int ld = p.d + 1;
-  float *sq = sm, *sk = sq + kR * ld, *sv = sk + kR * ld, *sp = sv + kR * ld;  // sp [kR][kR + 1]
+  extern __shared__ float4 smem4[];
+  float* sm = reinterpret_cast<float*>(smem4);
+  constexpr int kTile = kC * (D + 4);
+  float *sq = sm, *skv = sq + kR * (D + 4), *sp = skv + 4 * kTile;  // skv: K, V of two stages
   int d, tile;
   if (!block_tile(p.cu_q, p.n_docs, p.q_rows, d, tile)) return;
   const Doc doc = load_doc(p, d);
   const int h = blockIdx.y, hk = h / (p.H / p.Hk);
   const int i0 = tile * kR, rows = min(kR, doc.Lq - i0);
-  const int r = threadIdx.x >> 3, c = threadIdx.x & 7, i = i0 + r;
-  const int seen = r < rows ? seen_keys(i, doc.off, doc.Lk, doc.prefix, p.causal_block) : 0;
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const int most = seen_keys(i0 + rows - 1, doc.off, doc.Lk, doc.prefix, p.causal_block);
   const float slope = p.slopes ? p.slopes[h] : 0.f;
-  load_tile<T>(sq, p.q, p.q_stride, doc.q0 + i0, rows, h * p.d, p.d);
-  float m = -INFINITY, l = 0.f, o[kMaxD / 8] = {};
-  for (int j0 = 0; j0 < most; j0 += kR) {
-    __syncthreads();
-    const int keys = min(kR, doc.Lk - j0);
-    load_tile<T>(sk, p.k, p.k_stride, static_cast<int64_t>(doc.k0) + j0, keys, hk * p.d, p.d);
-    load_tile<T>(sv, p.v, p.v_stride, static_cast<int64_t>(doc.k0) + j0, keys, hk * p.d, p.d);
-    __syncthreads();
-    float s[4], mx = -INFINITY, turn;
+  auto load = [&](int j0, int stage) {
+    const int keys = min(kC, doc.Lk - j0);
+    load_async<D>(skv + 2 * stage * kTile, p.k, p.k_stride, static_cast<int64_t>(doc.k0) + j0, kC, keys, hk * p.d, p.d);
+    load_async<D>(skv + (2 * stage + 1) * kTile, p.v, p.v_stride, static_cast<int64_t>(doc.k0) + j0, kC, keys, hk * p.d, p.d);
+    async_commit();
+  };
+  load_async<D>(sq, p.q, p.q_stride, doc.q0 + i0, kR, rows, h * p.d, p.d);
+  if (most > 0) load(0, 0);
+  int seen[2];
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float4 o[2][D / 64] = {};
 #pragma unroll
-    for (int jj = 0; jj < 4; ++jj) {
-      const int j = c + 8 * jj;
-      s[jj] = j0 + j < seen ? score(dot_rows(sq + r * ld, sk + j * ld, p.d), p, slope, i + doc.off, j0 + j, turn) : -INFINITY;
-      mx = fmaxf(mx, s[jj]);
-    }
-    const float m_new = fmaxf(m, max8(mx));
-    const float base = m_new == -INFINITY ? 0.f : m_new;  // a row that has seen nothing yet
-    const float alpha = expf(m - base);
-    float sum = 0.f;
+  for (int i = 0; i < 2; ++i)
+    seen[i] = 2 * ty + i < rows ? seen_keys(i0 + 2 * ty + i, doc.off, doc.Lk, doc.prefix, p.causal_block) : 0;
+  for (int j0 = 0, st = 0; j0 < most; j0 += kC, st ^= 1) {
+    async_wait_all();
+    __syncthreads();  // this tile is there; the other stage has been read
+    if (j0 + kC < most) load(j0 + kC, st ^ 1);
+    float s[2][2];
+    dot_2x2<D>(sq, skv + 2 * st * kTile, s);
 #pragma unroll
-    for (int jj = 0; jj < 4; ++jj) {
-      const float e = expf(s[jj] - base);
-      sp[r * (kR + 1) + c + 8 * jj] = e;
-      sum += e;
-    }
-    l = l * alpha + sum8(sum);
-    m = m_new;
-    __syncwarp();
+    for (int i = 0; i < 2; ++i) {
+      float turn, mx = -INFINITY;
 #pragma unroll
-    for (int x = 0; x < kMaxD / 8; ++x)
-      if (c + 8 * x < p.d) {
-        float a = o[x] * alpha;
-        for (int j = 0; j < keys; ++j) a = fmaf(sp[r * (kR + 1) + j], sv[j * ld + c + 8 * x], a);
-        o[x] = a;
+      for (int j = 0; j < 2; ++j) {
+        const int key = j0 + tx + 16 * j;
+        s[i][j] = key < seen[i] ? score(s[i][j], p, slope, i0 + 2 * ty + i + doc.off, key, turn) : -INFINITY;
+        mx = fmaxf(mx, s[i][j]);
       }
-    __syncwarp();
-  }
-  if (r >= rows) return;
-  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN passes
-  T* out = static_cast<T*>(p.o) + static_cast<int64_t>(doc.q0 + i) * p.o_stride + h * p.d;
+      const float m_new = fmaxf(m[i], max16(mx));
+      const float base = m_new == -INFINITY ? 0.f : m_new;  // a row that has seen nothing yet
+      const float alpha = expf(m[i] - base);
+      const float e0 = expf(s[i][0] - base), e1 = expf(s[i][1] - base);
+      sp[(2 * ty + i) * kSp + tx] = e0;
+      sp[(2 * ty + i) * kSp + tx + 16] = e1;
+      l[i] = l[i] * alpha + sum16(e0 + e1);
+      m[i] = m_new;
 #pragma unroll
-  for (int x = 0; x < kMaxD / 8; ++x)
-    if (c + 8 * x < p.d) out[c + 8 * x] = from_f32<T>(o[x] * inv);
-  if (p.lse && c == 0) p.lse[static_cast<int64_t>(h) * p.q_rows + doc.q0 + i] = l == 0.f ? -INFINITY : m + logf(l);
+      for (int k = 0; k < D / 64; ++k) o[i][k].x *= alpha, o[i][k].y *= alpha, o[i][k].z *= alpha, o[i][k].w *= alpha;
+    }
+    __syncwarp();  // two rows of sp belong to one half-warp
+    add_product<D>(sp, skv + (2 * st + 1) * kTile, o);
+  }
+  async_wait_all();
+  float inv[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    inv[i] = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : l[i]);  // NaN passes
+    if (p.lse && tx == 0 && 2 * ty + i < rows)
+      p.lse[static_cast<int64_t>(h) * p.q_rows + doc.q0 + i0 + 2 * ty + i] = l[i] == 0.f ? -INFINITY : m[i] + logf(l[i]);
+  }
+  store_rows<D>(p.o, p.o_stride, static_cast<int64_t>(doc.q0) + i0, rows, h * p.d, p.d, o, inv);
 }
 
-// delta[h, row] = sum(do * o), one warp per (row, head).
-template <typename T>
+// dq, and delta of the block's rows for the other kernel.
+template <int D>
+__global__ void __launch_bounds__(kThreads) packed_dq_kernel(const PackedAttn p) {
+  extern __shared__ float4 smem4[];
+  float* sm = reinterpret_cast<float*>(smem4);
+  constexpr int kTile = kC * (D + 4);
+  float *sq = sm, *so = sq + kR * (D + 4), *skv = so + kR * (D + 4), *sp = skv + 4 * kTile;
+  int d, tile;
+  if (!block_tile(p.cu_q, p.n_docs, p.q_rows, d, tile)) return;
+  const Doc doc = load_doc(p, d);
+  const int h = blockIdx.y, hk = h / (p.H / p.Hk);
+  const int i0 = tile * kR, rows = min(kR, doc.Lq - i0);
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  const int most = seen_keys(i0 + rows - 1, doc.off, doc.Lk, doc.prefix, p.causal_block);
+  const float slope = p.slopes ? p.slopes[h] : 0.f;
+  auto load = [&](int j0, int stage) {
+    const int keys = min(kC, doc.Lk - j0);
+    load_async<D>(skv + 2 * stage * kTile, p.k, p.k_stride, static_cast<int64_t>(doc.k0) + j0, kC, keys, hk * p.d, p.d);
+    load_async<D>(skv + (2 * stage + 1) * kTile, p.v, p.v_stride, static_cast<int64_t>(doc.k0) + j0, kC, keys, hk * p.d, p.d);
+    async_commit();
+  };
+  load_async<D>(sq, p.q, p.q_stride, doc.q0 + i0, kR, rows, h * p.d, p.d);
+  load_async<D>(so, p.d_o, p.do_stride, doc.q0 + i0, kR, rows, h * p.d, p.d);
+  if (most > 0) load(0, 0);
+  int seen[2];
+  float lse[2], delta[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = 2 * ty + i;
+    float x = 0.f;
+    seen[i] = 0, lse[i] = 0.f;
+    if (r < rows) {
+      const int64_t row = static_cast<int64_t>(doc.q0) + i0 + r;
+      seen[i] = seen_keys(i0 + r, doc.off, doc.Lk, doc.prefix, p.causal_block);
+      if (seen[i] > 0) lse[i] = p.lse[static_cast<int64_t>(h) * p.q_rows + row];
+      for (int c = 4 * tx; c < p.d; c += 64) {
+        const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p.o) + row * p.o_stride + h * p.d + c);
+        const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(p.d_o) + row * p.do_stride + h * p.d + c);
+        x = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, x))));
+      }
+    }
+    delta[i] = sum16(x);
+    if (r < rows && tx == 0) p.delta[static_cast<int64_t>(h) * p.q_rows + doc.q0 + i0 + r] = delta[i];
+  }
+  float4 g[2][D / 64] = {};
+  for (int j0 = 0, st = 0; j0 < most; j0 += kC, st ^= 1) {
+    async_wait_all();
+    __syncthreads();
+    if (j0 + kC < most) load(j0 + kC, st ^ 1);
+    float s[2][2], dp[2][2];
+    dot_2x2<D>(sq, skv + 2 * st * kTile, s);
+    dot_2x2<D>(so, skv + (2 * st + 1) * kTile, dp);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int key = j0 + tx + 16 * j;
+        float ds = 0.f;
+        if (key < seen[i]) {
+          float turn;
+          const float z = score(s[i][j], p, slope, i0 + 2 * ty + i + doc.off, key, turn);
+          ds = expf(z - lse[i]) * (dp[i][j] - delta[i]) * turn;
+        }
+        sp[(2 * ty + i) * kSp + tx + 16 * j] = ds;
+      }
+    __syncwarp();
+    add_product<D>(sp, skv + 2 * st * kTile, g);
+  }
+  async_wait_all();
+  const float f[2] = {p.scale, p.scale};
+  store_rows<D>(p.dq, p.dq_stride, static_cast<int64_t>(doc.q0) + i0, rows, h * p.d, p.d, g, f);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) packed_dkv_kernel(const PackedAttn p) {
+  extern __shared__ float4 smem4[];
+  float* sm = reinterpret_cast<float*>(smem4);
+  constexpr int kTile = kC * (D + 4);
+  float *sk = sm, *sv = sk + kR * (D + 4), *sqo = sv + kR * (D + 4), *sp = sqo + 4 * kTile, *ss = sp + kR * kSp;
+  int d, tile;
+  if (!block_tile(p.cu_k, p.n_docs, p.k_rows, d, tile)) return;
+  const Doc doc = load_doc(p, d);
+  const int hk = blockIdx.y, group = p.H / p.Hk;
+  const int j0 = tile * kR, keys = min(kR, doc.Lk - j0);
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  const int first = first_query(j0, doc.off, doc.Lk, doc.prefix, p.causal_block);
+  const int per_head = first < doc.Lq ? (doc.Lq - first + kC - 1) / kC : 0, n = per_head * group;
+  auto load = [&](int t, int stage) {
+    const int h = hk * group + t / per_head, i0 = first + t % per_head * kC, rows = min(kC, doc.Lq - i0);
+    load_async<D>(sqo + 2 * stage * kTile, p.q, p.q_stride, static_cast<int64_t>(doc.q0) + i0, kC, rows, h * p.d, p.d);
+    load_async<D>(sqo + (2 * stage + 1) * kTile, p.d_o, p.do_stride, static_cast<int64_t>(doc.q0) + i0, kC, rows, h * p.d, p.d);
+    async_commit();
+  };
+  load_async<D>(sk, p.k, p.k_stride, static_cast<int64_t>(doc.k0) + j0, kR, keys, hk * p.d, p.d);
+  load_async<D>(sv, p.v, p.v_stride, static_cast<int64_t>(doc.k0) + j0, kR, keys, hk * p.d, p.d);
+  if (n > 0) load(0, 0);
+  float4 gk[2][D / 64] = {}, gv[2][D / 64] = {};
+  for (int t = 0, st = 0; t < n; ++t, st ^= 1) {
+    const int h = hk * group + t / per_head, i0 = first + t % per_head * kC;
+    const float slope = p.slopes ? p.slopes[h] : 0.f;
+    float lse[2], delta[2];
+    int seen[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int i = i0 + tx + 16 * x;
+      seen[x] = 0, lse[x] = delta[x] = 0.f;
+      if (i < doc.Lq) {
+        const int64_t stat = static_cast<int64_t>(h) * p.q_rows + doc.q0 + i;
+        seen[x] = seen_keys(i, doc.off, doc.Lk, doc.prefix, p.causal_block);
+        lse[x] = p.lse[stat], delta[x] = p.delta[stat];
+      }
+    }
+    async_wait_all();
+    __syncthreads();
+    if (t + 1 < n) load(t + 1, st ^ 1);
+    float s[2][2], dp[2][2];
+    dot_2x2<D>(sk, sqo + 2 * st * kTile, s);
+    dot_2x2<D>(sv, sqo + (2 * st + 1) * kTile, dp);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int key = j0 + 2 * ty + i;
+        float pr = 0.f, ds = 0.f;
+        if (2 * ty + i < keys && key < seen[x]) {
+          float turn;
+          const float z = score(s[i][x], p, slope, i0 + tx + 16 * x + doc.off, key, turn);
+          pr = expf(z - lse[x]);
+          ds = pr * (dp[i][x] - delta[x]) * turn;
+        }
+        sp[(2 * ty + i) * kSp + tx + 16 * x] = pr;
+        ss[(2 * ty + i) * kSp + tx + 16 * x] = ds;
+      }
+    __syncwarp();
+    add_product<D>(sp, sqo + (2 * st + 1) * kTile, gv);
+    add_product<D>(ss, sqo + 2 * st * kTile, gk);
+  }
+  async_wait_all();
+  const float one[2] = {1.f, 1.f}, f[2] = {p.scale, p.scale};
+  store_rows<D>(p.dk, p.dk_stride, static_cast<int64_t>(doc.k0) + j0, keys, hk * p.d, p.d, gk, f);
+  store_rows<D>(p.dv, p.dv_stride, static_cast<int64_t>(doc.k0) + j0, keys, hk * p.d, p.d, gv, one);
+}
+
+// delta[h, row] = sum(do * o) of bf16 rows (for the tensor-core gradient), one warp per (row, head).
 __global__ void __launch_bounds__(256) packed_delta_kernel(const PackedAttn p) {
   const int64_t w = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   const int64_t row = w / p.H;
   const int h = static_cast<int>(w - row * p.H);
   if (row >= p.q_rows) return;
-  const T* a = static_cast<const T*>(p.d_o) + row * p.do_stride + h * p.d;
-  const T* b = static_cast<const T*>(p.o) + row * p.o_stride + h * p.d;
+  const __nv_bfloat16* a = static_cast<const __nv_bfloat16*>(p.d_o) + row * p.do_stride + h * p.d;
+  const __nv_bfloat16* b = static_cast<const __nv_bfloat16*>(p.o) + row * p.o_stride + h * p.d;
   float s = 0.f;
-  for (int c = lane; c < p.d; c += 32) s = fmaf(to_f32<T>(a[c]), to_f32<T>(b[c]), s);
+  for (int c = 4 * lane; c < p.d; c += 128) {
+    const uint2 x = *reinterpret_cast<const uint2*>(a + c), y = *reinterpret_cast<const uint2*>(b + c);
+    s = fmaf(bf16_lo(x.x), bf16_lo(y.x), fmaf(bf16_hi(x.x), bf16_hi(y.x), fmaf(bf16_lo(x.y), bf16_lo(y.y), fmaf(bf16_hi(x.y), bf16_hi(y.y), s))));
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if (lane == 0) p.delta[static_cast<int64_t>(h) * p.q_rows + row] = s;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) packed_dq_kernel(const PackedAttn p) {
-  extern __shared__ float sm[];
-  const int ld = p.d + 1;
-  float *sq = sm, *so = sq + kR * ld, *sk = so + kR * ld, *sv = sk + kR * ld, *sp = sv + kR * ld;
-  int d, tile;
-  if (!block_tile(p.cu_q, p.n_docs, p.q_rows, d, tile)) return;
-  const Doc doc = load_doc(p, d);
-  const int h = blockIdx.y, hk = h / (p.H / p.Hk);
-  const int i0 = tile * kR, rows = min(kR, doc.Lq - i0);
-  const int r = threadIdx.x >> 3, c = threadIdx.x & 7, i = i0 + r;
-  const int seen = r < rows ? seen_keys(i, doc.off, doc.Lk, doc.prefix, p.causal_block) : 0;
-  const int most = seen_keys(i0 + rows - 1, doc.off, doc.Lk, doc.prefix, p.causal_block);
-  const float slope = p.slopes ? p.slopes[h] : 0.f;
-  load_tile<T>(sq, p.q, p.q_stride, doc.q0 + i0, rows, h * p.d, p.d);
-  load_tile<T>(so, p.d_o, p.do_stride, doc.q0 + i0, rows, h * p.d, p.d);
-  const int64_t stat = static_cast<int64_t>(h) * p.q_rows + doc.q0 + i;
-  const float lse = seen > 0 ? p.lse[stat] : 0.f, delta = seen > 0 ? p.delta[stat] : 0.f;
-  float g[kMaxD / 8] = {};
-  for (int j0 = 0; j0 < most; j0 += kR) {
-    __syncthreads();
-    const int keys = min(kR, doc.Lk - j0);
-    load_tile<T>(sk, p.k, p.k_stride, static_cast<int64_t>(doc.k0) + j0, keys, hk * p.d, p.d);
-    load_tile<T>(sv, p.v, p.v_stride, static_cast<int64_t>(doc.k0) + j0, keys, hk * p.d, p.d);
-    __syncthreads();
-#pragma unroll
-    for (int jj = 0; jj < 4; ++jj) {
-      const int j = c + 8 * jj;
-      float ds = 0.f;
-      if (j0 + j < seen) {
-        float turn;
-        const float s = score(dot_rows(sq + r * ld, sk + j * ld, p.d), p, slope, i + doc.off, j0 + j, turn);
-        ds = expf(s - lse) * (dot_rows(so + r * ld, sv + j * ld, p.d) - delta) * turn * p.scale;
-      }
-      sp[r * (kR + 1) + j] = ds;
-    }
-    __syncwarp();
-#pragma unroll
-    for (int x = 0; x < kMaxD / 8; ++x)
-      if (c + 8 * x < p.d)
-        for (int j = 0; j < keys; ++j) g[x] = fmaf(sp[r * (kR + 1) + j], sk[j * ld + c + 8 * x], g[x]);
-    __syncwarp();
-  }
-  if (r >= rows) return;
-  T* out = static_cast<T*>(p.dq) + static_cast<int64_t>(doc.q0 + i) * p.dq_stride + h * p.d;
-#pragma unroll
-  for (int x = 0; x < kMaxD / 8; ++x)
-    if (c + 8 * x < p.d) out[c + 8 * x] = from_f32<T>(g[x]);
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) packed_dkv_kernel(const PackedAttn p) {
-  extern __shared__ float sm[];
-  const int ld = p.d + 1;
-  float *sk = sm, *sv = sk + kR * ld, *sq = sv + kR * ld, *so = sq + kR * ld, *sp = so + kR * ld, *ss = sp + kR * (kR + 1);
-  int d, tile;
-  if (!block_tile(p.cu_k, p.n_docs, p.k_rows, d, tile)) return;
-  const Doc doc = load_doc(p, d);
-  const int hk = blockIdx.y, group = p.H / p.Hk;
-  const int j0 = tile * kR, keys = min(kR, doc.Lk - j0);
-  const int r = threadIdx.x >> 3, c = threadIdx.x & 7, j = j0 + r;
-  load_tile<T>(sk, p.k, p.k_stride, static_cast<int64_t>(doc.k0) + j0, keys, hk * p.d, p.d);
-  load_tile<T>(sv, p.v, p.v_stride, static_cast<int64_t>(doc.k0) + j0, keys, hk * p.d, p.d);
-  const int first = first_query(j0, doc.off, doc.Lk, doc.prefix, p.causal_block);
-  float gk[kMaxD / 8] = {}, gv[kMaxD / 8] = {};
-  for (int h = hk * group; h < (hk + 1) * group; ++h) {
-    const float slope = p.slopes ? p.slopes[h] : 0.f;
-    for (int i0 = first; i0 < doc.Lq; i0 += kR) {
-      __syncthreads();
-      const int rows = min(kR, doc.Lq - i0);
-      load_tile<T>(sq, p.q, p.q_stride, static_cast<int64_t>(doc.q0) + i0, rows, h * p.d, p.d);
-      load_tile<T>(so, p.d_o, p.do_stride, static_cast<int64_t>(doc.q0) + i0, rows, h * p.d, p.d);
-      __syncthreads();
-#pragma unroll
-      for (int ii = 0; ii < 4; ++ii) {
-        const int x = c + 8 * ii, i = i0 + x;
-        float pr = 0.f, ds = 0.f;
-        if (x < rows && r < keys && j < seen_keys(i, doc.off, doc.Lk, doc.prefix, p.causal_block)) {
-          const int64_t stat = static_cast<int64_t>(h) * p.q_rows + doc.q0 + i;
-          float turn;
-          const float s = score(dot_rows(sk + r * ld, sq + x * ld, p.d), p, slope, i + doc.off, j, turn);
-          pr = expf(s - p.lse[stat]);
-          ds = pr * (dot_rows(sv + r * ld, so + x * ld, p.d) - p.delta[stat]) * turn * p.scale;
-        }
-        sp[r * (kR + 1) + x] = pr;
-        ss[r * (kR + 1) + x] = ds;
-      }
-      __syncwarp();
-#pragma unroll
-      for (int x = 0; x < kMaxD / 8; ++x)
-        if (c + 8 * x < p.d)
-          for (int y = 0; y < rows; ++y) {
-            gv[x] = fmaf(sp[r * (kR + 1) + y], so[y * ld + c + 8 * x], gv[x]);
-            gk[x] = fmaf(ss[r * (kR + 1) + y], sq[y * ld + c + 8 * x], gk[x]);
-          }
-      __syncwarp();
-    }
-  }
-  if (r >= keys) return;
-  T* ok = static_cast<T*>(p.dk) + static_cast<int64_t>(doc.k0 + j) * p.dk_stride + hk * p.d;
-  T* ov = static_cast<T*>(p.dv) + static_cast<int64_t>(doc.k0 + j) * p.dv_stride + hk * p.d;
-#pragma unroll
-  for (int x = 0; x < kMaxD / 8; ++x)
-    if (c + 8 * x < p.d) {
-      ok[c + 8 * x] = from_f32<T>(gk[x]);
-      ov[c + 8 * x] = from_f32<T>(gv[x]);
-    }
-}
-
-size_t tile_bytes(int d, int tiles, int squares) {
-  return (static_cast<size_t>(tiles) * kR * (d + 1) + static_cast<size_t>(squares) * kR * (kR + 1)) * sizeof(float);
-}
-
 // At most this many tiles: every document adds less than one partial tile.
 unsigned most_tiles(int rows, int n_docs) { return static_cast<unsigned>(rows / kR) + static_cast<unsigned>(n_docs); }
 
-template <typename K>
-void allow_smem(K kernel, size_t bytes) {
-  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+// Shared memory of a block: `own` tiles of its rows, two stages of two tiles, `squares` of
+// probabilities.
+template <int D>
+constexpr size_t smem_bytes(int own, int squares) {
+  return (static_cast<size_t>(own * kR + 4 * kC) * (D + 4) + static_cast<size_t>(squares) * kR * kSp) * sizeof(float);
 }
-
-template <typename T>
-int fwd(const PackedAttn& p, cudaStream_t s) {
-  const size_t sm = tile_bytes(p.d, 3, 1);
-  allow_smem(packed_fwd_kernel<T>, sm);
-  packed_fwd_kernel<T><<<dim3(most_tiles(p.q_rows, p.n_docs), p.H), kThreads, sm, s>>>(p);
+template <typename K>
+int launch(K kernel, size_t smem, dim3 grid, const PackedAttn& p, cudaStream_t s) {
+  if (smem > 48 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  kernel<<<grid, kThreads, smem, s>>>(p);
   return check_launch();
 }
-template <typename T>
+template <int D>
+int fwd(const PackedAttn& p, cudaStream_t s) {
+  return launch(packed_fwd_kernel<D>, smem_bytes<D>(1, 1), dim3(most_tiles(p.q_rows, p.n_docs), p.H), p, s);
+}
+template <int D>
+int bwd(const PackedAttn& p, cudaStream_t s) {
+  int st = WAN_OK, launched = 0;
+  if (p.q_rows > 0) {
+    st = launch(packed_dq_kernel<D>, smem_bytes<D>(2, 1), dim3(most_tiles(p.q_rows, p.n_docs), p.H), p, s);
+    ++launched;
+  }
+  if (st == WAN_OK && p.k_rows > 0) {
+    st = launch(packed_dkv_kernel<D>, smem_bytes<D>(2, 2), dim3(most_tiles(p.k_rows, p.n_docs), p.Hk), p, s);
+    ++launched;
+  }
+  count_launches(launched - 1);
+  return st;
+}
 int delta(const PackedAttn& p, cudaStream_t s) {
   if (p.q_rows == 0) {
     count_launches(-1);
     return WAN_OK;
   }
   const int64_t warps = static_cast<int64_t>(p.q_rows) * p.H;
-  packed_delta_kernel<T><<<static_cast<unsigned>((warps + 7) / 8), 256, 0, s>>>(p);
+  packed_delta_kernel<<<static_cast<unsigned>((warps + 7) / 8), 256, 0, s>>>(p);
   return check_launch();
-}
-template <typename T>
-int bwd(const PackedAttn& p, cudaStream_t s) {
-  int st = WAN_OK;
-  if (p.q_rows > 0) {
-    const size_t sm = tile_bytes(p.d, 4, 1);
-    allow_smem(packed_dq_kernel<T>, sm);
-    packed_dq_kernel<T><<<dim3(most_tiles(p.q_rows, p.n_docs), p.H), kThreads, sm, s>>>(p);
-    count_launches(1);
-    st = check_launch();
-  }
-  if (st == WAN_OK && p.k_rows > 0) {
-    const size_t sm = tile_bytes(p.d, 4, 2);
-    allow_smem(packed_dkv_kernel<T>, sm);
-    packed_dkv_kernel<T><<<dim3(most_tiles(p.k_rows, p.n_docs), p.Hk), kThreads, sm, s>>>(p);
-    count_launches(1);
-    st = check_launch();
-  }
-  return st;
 }
 
 }  // namespace
 
 int launch_attn_packed_simt(const PackedAttn& p, cudaStream_t s) {
   trace_launch_begin(WAN_KIND_ATTN, s);
-  const int st = fwd<float>(p, s);
+  const int st = p.d <= 64 ? fwd<64>(p, s) : fwd<128>(p, s);
   trace_launch_end(WAN_KIND_ATTN, s);
   return st;
 }
 
 int launch_attn_packed_bwd(const PackedAttn& p, int dtype, cudaStream_t s) {
   trace_launch_begin(WAN_KIND_ATTN, s);
-  int st = dtype == WAN_BF16 ? delta<__nv_bfloat16>(p, s) : delta<float>(p, s);
-  if (st == WAN_OK) st = dtype == WAN_BF16 ? launch_attn_packed_tc_bwd(p, s) : bwd<float>(p, s);
+  int st = WAN_OK;
+  if (dtype == WAN_BF16) {
+    st = delta(p, s);
+    if (st == WAN_OK) st = launch_attn_packed_tc_bwd(p, s);
+  } else {
+    st = p.d <= 64 ? bwd<64>(p, s) : bwd<128>(p, s);
+  }
   trace_launch_end(WAN_KIND_ATTN, s);
   return st;
 }
