@@ -150,40 +150,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && n > 0) {
+    const int nu = uniform(n);
+    if (nu > 0) {
       const uint32_t id_kk = idesc_bf16_f32(kPkTile, kPkTile, 0, 0), id_mn = idesc_bf16_f32(kPkTile, kPkD, 0, 1);
+      const uint32_t tm = uniform(tmem);
       const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024), o_desc = sdesc_sw128(smem_u32(sQ + kPkTileBytes), 16, 1024);
       const uint64_t kv_desc = sdesc_sw128(smem_u32(sKV), 16, 1024), kt_desc = sdesc_sw128(smem_u32(sKV), kPkSpan, 1024);
       auto stage_off = [](int pos) { return static_cast<uint32_t>((pos % kDqStages * kPkTileBytes) >> 4); };
       auto wait_pos = [&](int pos) {
-        return mbar_wait(&kv_full[pos % kDqStages], static_cast<uint32_t>((pos / kDqStages) & 1), p.err);
+        return mbar_wait_warp(&kv_full[pos % kDqStages], static_cast<uint32_t>((pos / kDqStages) & 1), p.err);
       };
       // S(j), then dP(j) once dP(j-1) has been read
       auto scores = [&](int j) {
         if (!wait_pos(2 * j)) return false;
-        if (j == n - 1 && end < kPkTile) {
-          mbar_arrive(ragged);
-          if (!mbar_wait(cleared, 0, p.err)) return false;
+        if (j == nu - 1 && uniform(end) < kPkTile) {
+          if (lane == 0) mbar_arrive(ragged);
+          if (!mbar_wait_warp(cleared, 0, p.err)) return false;
         }
-        mma_ss(tmem + 128 * (j & 1), q_desc, kv_desc + stage_off(2 * j), id_kk);
+        const uint64_t kd = kv_desc + stage_off(2 * j), vd = kv_desc + stage_off(2 * j + 1);
+        if (elect_lane()) mma_ss(tm + 128 * (j & 1), q_desc, kd, id_kk);
         if (!wait_pos(2 * j + 1)) return false;
-        if (j > 0 && !mbar_wait(y_free, static_cast<uint32_t>((j - 1) & 1), p.err)) return false;
+        if (j > 0 && !mbar_wait_warp(y_free, static_cast<uint32_t>((j - 1) & 1), p.err)) return false;
         tc_fence_after();
-        mma_ss(Y, o_desc, kv_desc + stage_off(2 * j + 1), id_kk);
-        tc_commit(&kv_empty[(2 * j + 1) % kDqStages]);
-        tc_commit(s_full);
+        if (elect_lane()) {
+          mma_ss(tm + 256, o_desc, vd, id_kk);
+          tc_commit(&kv_empty[(2 * j + 1) % kDqStages]);
+          tc_commit(s_full);
+        }
         return true;
       };
-      bool ok = mbar_wait(q_full, 0, p.err) && scores(0);
-      for (int j = 0; ok && j < n; ++j) {
-        if (j + 1 < n && !scores(j + 1)) break;
-        if (!mbar_wait(ds_full, static_cast<uint32_t>(j & 1), p.err)) break;
+      bool ok = mbar_wait_warp(q_full, 0, p.err) && scores(0);
+      for (int j = 0; ok && j < nu; ++j) {
+        if (j + 1 < nu && !scores(j + 1)) break;
+        if (!mbar_wait_warp(ds_full, static_cast<uint32_t>(j & 1), p.err)) break;
         tc_fence_after();
-        mma_ts_halves(Z, tmem + 128 * (j & 1), kt_desc + stage_off(2 * j), id_mn, j == 0);
-        tc_commit(&kv_empty[2 * j % kDqStages]);
+        const uint64_t kd = kt_desc + stage_off(2 * j);
+        if (elect_lane()) {
+          mma_ts_halves(tm + 384, tm + 128 * (j & 1), kd, id_mn, j == 0);
+          tc_commit(&kv_empty[2 * j % kDqStages]);
+        }
       }
-      tc_commit(done);
-      mbar_wait(done, 0, p.err);
+      if (elect_lane()) tc_commit(done);
+      mbar_wait_warp(done, 0, p.err);
     }
   } else if (warp == 3) {
     if (n > 0 && end < kPkTile && mbar_wait_warp(ragged, 0, p.err)) {
@@ -385,49 +393,57 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && w.n > 0) {
+    const int nu = uniform(w.n), per_group = uniform(w.per_group);
+    if (nu > 0) {
       const uint32_t id_kk = idesc_bf16_f32(kPkTile, kPkTile, 0, 0), id_mn = idesc_bf16_f32(kPkTile, kPkD, 0, 1);
+      const uint32_t tm = uniform(tmem);
       const uint64_t k_desc = sdesc_sw128(smem_u32(sKV), 16, 1024), v_desc = sdesc_sw128(smem_u32(sKV + kPkTileBytes), 16, 1024);
       const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024), qt_desc = sdesc_sw128(smem_u32(sQ), kPkSpan, 1024);
       auto stage_off = [](int pos) { return static_cast<uint32_t>((pos % kDkvStages * kPkTileBytes) >> 4); };
       auto wait_pos = [&](int pos) {
-        return mbar_wait(&q_full[pos % kDkvStages], static_cast<uint32_t>((pos / kDkvStages) & 1), p.err);
+        return mbar_wait_warp(&q_full[pos % kDkvStages], static_cast<uint32_t>((pos / kDkvStages) & 1), p.err);
       };
       int ragged_seen = 0;
+      const bool ragged_end = uniform(last_rows) < used;
       // Tile i is there, its rows behind the document's end cleared.
       auto arrived = [&](int i) {
         if (!wait_pos(2 * i) || !wait_pos(2 * i + 1)) return false;
-        if (last_rows < used && (i + 1) % w.per_group == 0) {
-          mbar_arrive(ragged);
-          if (!mbar_wait(cleared, static_cast<uint32_t>(ragged_seen++ & 1), p.err)) return false;
+        if (ragged_end && (i + 1) % per_group == 0) {
+          if (lane == 0) mbar_arrive(ragged);
+          if (!mbar_wait_warp(cleared, static_cast<uint32_t>(ragged_seen++ & 1), p.err)) return false;
         }
         return true;
       };
-      bool ok = mbar_wait(kv_full, 0, p.err) && arrived(0);
-      if (ok) {
-        mma_ss(tmem, k_desc, q_desc + stage_off(0), id_kk);
-        mma_ss(Y, v_desc, q_desc + stage_off(1), id_kk);
+      bool ok = mbar_wait_warp(kv_full, 0, p.err) && arrived(0);
+      if (ok && elect_lane()) {
+        mma_ss(tm, k_desc, q_desc, id_kk);
+        mma_ss(tm + 128, v_desc, q_desc + stage_off(1), id_kk);
         tc_commit(s_full);
       }
-      for (int i = 0; ok && i < w.n; ++i) {
-        if (i + 1 < w.n) {
-          if (!arrived(i + 1) || !mbar_wait(y_free, static_cast<uint32_t>(i & 1), p.err)) break;
+      for (int i = 0; ok && i < nu; ++i) {
+        const bool more = i + 1 < nu;
+        if (more) {
+          if (!arrived(i + 1) || !mbar_wait_warp(y_free, static_cast<uint32_t>(i & 1), p.err)) break;
           tc_fence_after();
-          mma_ss(Y, v_desc, q_desc + stage_off(2 * i + 3), id_kk);
+          const uint64_t od = q_desc + stage_off(2 * i + 3);
+          if (elect_lane()) mma_ss(tm + 128, v_desc, od, id_kk);
         }
-        if (!mbar_wait(p_full, static_cast<uint32_t>(i & 1), p.err)) break;
+        if (!mbar_wait_warp(p_full, static_cast<uint32_t>(i & 1), p.err)) break;
         tc_fence_after();
-        mma_ts_halves(dV, tmem, qt_desc + stage_off(2 * i + 1), id_mn, i == 0);
-        tc_commit(&q_empty[(2 * i + 1) % kDkvStages]);
-        mma_ts_halves(dK, tmem + 32, qt_desc + stage_off(2 * i), id_mn, i == 0);
-        tc_commit(&q_empty[2 * i % kDkvStages]);
-        if (i + 1 < w.n) {
-          mma_ss(tmem, k_desc, q_desc + stage_off(2 * i + 2), id_kk);
-          tc_commit(s_full);
+        const uint64_t od = qt_desc + stage_off(2 * i + 1), qd = qt_desc + stage_off(2 * i), next = q_desc + stage_off(2 * i + 2);
+        if (elect_lane()) {
+          mma_ts_halves(tm + 256, tm, od, id_mn, i == 0);
+          tc_commit(&q_empty[(2 * i + 1) % kDkvStages]);
+          mma_ts_halves(tm + 384, tm + 32, qd, id_mn, i == 0);
+          tc_commit(&q_empty[2 * i % kDkvStages]);
+          if (more) {
+            mma_ss(tm, k_desc, next, id_kk);
+            tc_commit(s_full);
+          }
         }
       }
-      tc_commit(done);
-      mbar_wait(done, 0, p.err);
+      if (elect_lane()) tc_commit(done);
+      mbar_wait_warp(done, 0, p.err);
     }
   } else if (warp == 2) {
     // The numbers of each query tile's columns. A column of no query, and a query that sees

@@ -7,7 +7,7 @@
 // threads, one CTA per SM, looping over its work):
 //   warp 0   : TMA loads: both Q tiles, then K_0, K_1, V_0, K_2, V_1, ... through a
 //              5-stage ring of 32 KB tiles;
-//   warp 1   : tcgen05.mma: for key tile j and query tile t, O_t += P_t(j-1) V_{j-1} with
+//   warp 1   : tcgen05.mma, issued by one lane: for key tile j and query tile t, O_t += P_t(j-1) V_{j-1} with
 //              P from tensor memory, then S_t = Q_t K_j^T;
 //   warp 3   : finds this CTA's share of the work, later clears ragged V tiles; warp 2 notes
 //              where the share ends;
@@ -408,93 +408,96 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (warp == 1) {
-      if (lane == 0) {
-        const uint32_t idesc_qk = idesc_bf16_f32(kPkTile, kPkTile, 0, 0), idesc_pv = idesc_bf16_f32(kPkTile, kPkD, 0, 1);
-        const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
-        const uint64_t k_desc = sdesc_sw128(smem_u32(sKV), 16, 1024);
-        const uint64_t v_desc = sdesc_sw128(smem_u32(sKV), kPkSpan, 1024);
-        auto wait_pos = [&](int pos) {
-          return mbar_wait(&kv_full[pos % kStages], static_cast<uint32_t>((pos / kStages) & 1), p.err);
-        };
-        auto pv = [&](int t, bool first, int stage) {
-          const uint64_t vd = v_desc + static_cast<uint32_t>((stage * kPkTileBytes) >> 4);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            tc_mma_bf16_ts(tmem_base + 256 + t * kPkTile, tmem_base + t * kPkTile + k * 8, vd + ((k * 16 * 128) >> 4),
-                           idesc_pv, (!first || k > 0) ? 1u : 0u);
-        };
-        auto qk = [&](int t, int stage) {
-          const uint64_t qd = q_desc + static_cast<uint32_t>((t * kPkTileBytes) >> 4);
-          const uint64_t kd = k_desc + static_cast<uint32_t>((stage * kPkTileBytes) >> 4);
+      const uint32_t idesc_qk = idesc_bf16_f32(kPkTile, kPkTile, 0, 0), idesc_pv = idesc_bf16_f32(kPkTile, kPkD, 0, 1);
+      const uint32_t tm = uniform(tmem_base);
+      const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t k_desc = sdesc_sw128(smem_u32(sKV), 16, 1024);
+      const uint64_t v_desc = sdesc_sw128(smem_u32(sKV), kPkSpan, 1024);
+      auto wait_pos = [&](int pos) {
+        return mbar_wait_warp(&kv_full[pos % kStages], static_cast<uint32_t>((pos / kStages) & 1), p.err);
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (elect_lane()) tc_commit(bar);
+      };
+      auto qk = [&](int t, int stage) {
+        const uint64_t qd = q_desc + static_cast<uint32_t>((t * kPkTileBytes) >> 4);
+        const uint64_t kd = k_desc + static_cast<uint32_t>((stage * kPkTileBytes) >> 4);
+        if (elect_lane()) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const uint32_t off = ((k >> 2) * kPkSpan + (k & 3) * 32) >> 4;
-            tc_mma_bf16(tmem_base + t * kPkTile, qd + off, kd + off, idesc_qk, k > 0 ? 1u : 0u);
+            tc_mma_bf16(tm + t * kPkTile, qd + off, kd + off, idesc_qk, k > 0 ? 1u : 0u);
           }
           tc_commit(&s_full[t]);
-        };
-        int base = 0, units = 0, ragged_seen = 0;
-        uint32_t seen0 = 0, seen1 = 0;  // key tiles whose P was waited for
-        // O_t += P_t V. The first product of a piece overwrites O_t: the softmax threads read
-        // the piece before out of it before they arrived on p_full for this one.
-        auto next_pv = [&](int t, uint32_t& seen, bool first, int stage) {
-          if (!mbar_wait(&p_full[t], seen & 1u, p.err)) return false;
-          ++seen;
-          tc_fence_after();
-          pv(t, first, stage);
-          return true;
-        };
-        bool ok = true;
-        while (ok && walk_step(walk, p, *share)) {
-          const int nmax = x.nmax, n0 = x.n[0], n1 = x.n[1];
-          if (nmax == 0) continue;
-          if (!mbar_wait(q_full, static_cast<uint32_t>(units & 1), p.err)) break;
-          ++units;
-          for (int j = 0; j < nmax; ++j) {
-            const int pk = base + pos_k(j), pvp = base + pos_v(j - 1, nmax);
-            const int ks = pk % kStages, vs = pvp % kStages;
-            ok = wait_pos(pk) && (j == 0 || wait_pos(pvp));
-            if (!ok) break;
-            if (j > 0 && j <= n0) {
-              ok = next_pv(0, seen0, j == 1, vs);
-              if (!ok) break;
-              if (j == n0) tc_commit(&o_final[0]);  // tile 0 ends before tile 1
-            }
-            if (j < n0) qk(0, ks);
-            if (j > 0 && j <= n1) {
-              ok = next_pv(1, seen1, j == 1, vs);
-              if (!ok) break;
-              if (j == n1) tc_commit(&o_final[1]);
-            }
-            if (j < n1) qk(1, ks);
-            tc_commit(&kv_empty[ks]);
-            if (j > 0) tc_commit(&kv_empty[vs]);
-          }
-          if (!ok) break;
-          tc_commit(q_empty);
-          const int pvp = base + pos_v(nmax - 1, nmax), vs = pvp % kStages;
-          if (!wait_pos(pvp)) break;
-          if (doc.Lk - (x.k0 + nmax - 1) * kPkTile < kPkTile) {
-            mbar_arrive(ragged);
-            if (!mbar_wait(cleared, static_cast<uint32_t>(ragged_seen & 1), p.err)) break;
-            ++ragged_seen;
-          }
-          if (n0 == nmax) {
-            ok = next_pv(0, seen0, nmax == 1, vs);
-            if (!ok) break;
-            tc_commit(&o_final[0]);
-          }
-          if (n1 == nmax) {
-            ok = next_pv(1, seen1, nmax == 1, vs);
-            if (!ok) break;
-            tc_commit(&o_final[1]);
-          }
-          tc_commit(&kv_empty[vs]);
-          base += 2 * nmax;
         }
-        tc_commit(drain);
-        mbar_wait(drain, 0, p.err);
+      };
+      int base = 0, units = 0, ragged_seen = 0;
+      uint32_t seen0 = 0, seen1 = 0;  // key tiles whose P was waited for
+      // O_t += P_t V. The first product of a piece overwrites O_t: the softmax threads read
+      // the piece before out of it before they arrived on p_full for this one.
+      auto next_pv = [&](int t, uint32_t& seen, bool first, int stage) {
+        if (!mbar_wait_warp(&p_full[t], seen & 1u, p.err)) return false;
+        ++seen;
+        tc_fence_after();
+        const uint64_t vd = v_desc + static_cast<uint32_t>((stage * kPkTileBytes) >> 4);
+        if (elect_lane()) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            tc_mma_bf16_ts(tm + 256 + t * kPkTile, tm + t * kPkTile + k * 8, vd + ((k * 16 * 128) >> 4), idesc_pv,
+                           (!first || k > 0) ? 1u : 0u);
+        }
+        return true;
+      };
+      bool ok = true;
+      while (ok && walk_next(walk, p, *share)) {
+        const int nmax = uniform(x.nmax), n0 = uniform(x.n[0]), n1 = uniform(x.n[1]);
+        if (nmax == 0) continue;
+        if (!mbar_wait_warp(q_full, static_cast<uint32_t>(units & 1), p.err)) break;
+        ++units;
+        for (int j = 0; j < nmax; ++j) {
+          const int pk = base + pos_k(j), pvp = base + pos_v(j - 1, nmax);
+          const int ks = pk % kStages, vs = pvp % kStages;
+          ok = wait_pos(pk) && (j == 0 || wait_pos(pvp));
+          if (!ok) break;
+          if (j > 0 && j <= n0) {
+            ok = next_pv(0, seen0, j == 1, vs);
+            if (!ok) break;
+            if (j == n0) commit(&o_final[0]);  // tile 0 ends before tile 1
+          }
+          if (j < n0) qk(0, ks);
+          if (j > 0 && j <= n1) {
+            ok = next_pv(1, seen1, j == 1, vs);
+            if (!ok) break;
+            if (j == n1) commit(&o_final[1]);
+          }
+          if (j < n1) qk(1, ks);
+          commit(&kv_empty[ks]);
+          if (j > 0) commit(&kv_empty[vs]);
+        }
+        if (!ok) break;
+        commit(q_empty);
+        const int pvp = base + pos_v(nmax - 1, nmax), vs = pvp % kStages;
+        if (!wait_pos(pvp)) break;
+        if (uniform(doc.Lk - (x.k0 + nmax - 1) * kPkTile) < kPkTile) {
+          if (lane == 0) mbar_arrive(ragged);
+          if (!mbar_wait_warp(cleared, static_cast<uint32_t>(ragged_seen & 1), p.err)) break;
+          ++ragged_seen;
+        }
+        if (n0 == nmax) {
+          ok = next_pv(0, seen0, nmax == 1, vs);
+          if (!ok) break;
+          commit(&o_final[0]);
+        }
+        if (n1 == nmax) {
+          ok = next_pv(1, seen1, nmax == 1, vs);
+          if (!ok) break;
+          commit(&o_final[1]);
+        }
+        commit(&kv_empty[vs]);
+        base += 2 * nmax;
       }
+      commit(drain);
+      mbar_wait_warp(drain, 0, p.err);
     } else if (warp == 3) {
       int base = 0, ragged_seen = 0;
       while (walk_next(walk, p, *share)) {

@@ -26,6 +26,21 @@ __device__ __forceinline__ DocRows load_doc(const PackedAttn& p, int d) {
   return {a.first, a.count, b.first, b.count, b.count - a.count, p.prefix ? __ldg(p.prefix + d) : 0};
 }
 
+// The warp that issues tensor-core instructions runs as a whole, one elected lane issues. A
+// value that all its lanes share is taken from lane 0 by a shuffle: the compiler then knows
+// that it is uniform and forms addresses and descriptors from it in uniform registers, which
+// these instructions read. (From vector registers every operand of every instruction was moved
+// across; the forward spent 20 % more time per key tile.)
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+template <typename T>
+__device__ __forceinline__ T uniform(T v) {
+  return __shfl_sync(0xffffffffu, v, 0);
+}
+
 __device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
 
 // Zero rows [row0, 128) of a bf16 tile in shared memory, by one warp: rows behind a
