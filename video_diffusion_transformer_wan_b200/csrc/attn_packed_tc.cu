@@ -47,12 +47,18 @@ constexpr int kMaxCtas = 148;
 constexpr int kMinSplit = 8;         // a unit of more key tiles may be cut
 constexpr int kMinShare = 4;         // key tiles a CTA takes at least
 constexpr float kRescaleLog2 = 8.0f;
+constexpr int kPolyEvery = 8;        // one pair of exponentials in this many runs on the FMA pipes
 constexpr size_t kSmem = 1024 + static_cast<size_t>(kPkTileBytes) * (2 + kStages) + 2048;
 static_assert(kSmem <= 232448, "shared memory of an SM");
 
 // Where a CTA's share ends inside a unit that begins in it: what the merge needs.
 struct Cut {
   int crosses, first_slot, last_cta, row0, rows, group;
+};
+
+template <bool kV>
+struct BoolConstant {
+  static constexpr bool value = kV;
 };
 
 struct FwdParams {
@@ -321,14 +327,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* kv_empty = kv_full + kStages;
   uint64_t* s_full = kv_empty + kStages;     // [2]
   uint64_t* p_full = s_full + 2;             // [2]
-  uint64_t* o_final = p_full + 2;            // [2]
+  uint64_t* p_half = p_full + 2;             // [2]: its first 64 columns
+  uint64_t* o_final = p_half + 2;            // [2]
   uint64_t* ragged = o_final + 2;            // a ragged V tile has landed; its end is cleared
   uint64_t* cleared = ragged + 1;
   uint64_t* drain = ragged + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   Share* share = reinterpret_cast<Share*>(drain + 2);
 
-  static_assert(22 * 8 + sizeof(Share) + 12 * sizeof(Walk) <= 2048, "barriers and walks");
+  static_assert(24 * 8 + sizeof(Share) + 12 * sizeof(Walk) <= 2048, "barriers and walks");
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -341,6 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
       mbar_init(&p_full[t], 128);
+      mbar_init(&p_half[t], 128);
       mbar_init(&o_final[t], 1);
     }
     mbar_init(ragged, 1);
@@ -436,16 +444,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       // O_t += P_t V. The first product of a piece overwrites O_t: the softmax threads read
       // the piece before out of it before they arrived on p_full for this one.
       auto next_pv = [&](int t, uint32_t& seen, bool first, int stage) {
-        if (!mbar_wait_warp(&p_full[t], seen & 1u, p.err)) return false;
-        ++seen;
-        tc_fence_after();
         const uint64_t vd = v_desc + static_cast<uint32_t>((stage * kPkTileBytes) >> 4);
-        if (elect_lane()) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            tc_mma_bf16_ts(tm + 256 + t * kPkTile, tm + t * kPkTile + k * 8, vd + ((k * 16 * 128) >> 4), idesc_pv,
-                           (!first || k > 0) ? 1u : 0u);
+        for (int h = 0; h < 2; ++h) {
+          if (!mbar_wait_warp(h == 0 ? &p_half[t] : &p_full[t], seen & 1u, p.err)) return false;
+          tc_fence_after();
+          if (elect_lane()) {
+#pragma unroll
+            for (int k = 4 * h; k < 4 * h + 4; ++k)
+              tc_mma_bf16_ts(tm + 256 + t * kPkTile, tm + t * kPkTile + k * 8, vd + ((k * 16 * 128) >> 4), idesc_pv,
+                             (!first || k > 0) ? 1u : 0u);
+          }
         }
+        ++seen;
         return true;
       };
       bool ok = true;
@@ -566,7 +577,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < kPkTile; ++c)
             r[c] = __float_as_uint(fmaf(__uint_as_float(r[c]), p.mult, -slope2 * fabsf(from - static_cast<float>(c))));
         }
-        if (__any_sync(0xffffffffu, valid < kPkTile)) {
+        const bool cut = __any_sync(0xffffffffu, valid < kPkTile);
+        if (cut) {
 #pragma unroll
           for (int c = 0; c < kPkTile; ++c)
             if (c >= valid) r[c] = __float_as_uint(-INFINITY);
@@ -593,15 +605,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float nb = m_run == -INFINITY ? 0.f : -m_run * mult;  // a row that has seen nothing yet
         const unsigned long long mult2 = f2_pack(mult, mult), nb2 = f2_pack(nb, nb);
         unsigned long long rs4[4] = {0ull, 0ull, 0ull, 0ull};
+        // Masked entries are exactly 0 (the polynomial stops at 2^-125), so it is left out there.
+        auto exps = [&](int c0, auto poly) {
 #pragma unroll
-        for (int c = 0; c < kPkTile / 2; ++c) {
-          const float2 y = f2_unpack(f2_fma(f2_pack(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])), mult2, nb2));
-          const float e0 = ex2_approx(y.x), e1 = ex2_approx(y.y);
-          rs4[c & 3] = f2_add(rs4[c & 3], f2_pack(e0, e1));
-          r[c] = pack_bf16x2(e0, e1);
-        }
+          for (int c = c0; c < c0 + kPkTile / 4; ++c) {
+            const unsigned long long y2 = f2_fma(f2_pack(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])), mult2, nb2);
+            float2 e;
+            if (poly.value && c % kPolyEvery == kPolyEvery - 1) {
+              e = f2_unpack(exp2_poly2(y2));
+            } else {
+              const float2 y = f2_unpack(y2);
+              e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+            }
+            rs4[c & 3] = f2_add(rs4[c & 3], f2_pack(e.x, e.y));
+            r[c] = pack_bf16x2(e.x, e.y);
+          }
+        };
+        if (cut)
+          exps(0, BoolConstant<false>{});
+        else
+          exps(0, BoolConstant<true>{});
         tmem_st32(s_row, *reinterpret_cast<uint32_t(*)[32]>(r));
-        tmem_st32(s_row + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
         if (rescale) {
           // S_t(j) ready implies that PV_t(j-1) completed, and PV_t(j) waits for this
           // thread's arrival below: O_t is current and idle here.
@@ -616,6 +640,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           l_run *= alpha;
         }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&p_half[t]);  // the product over the first 64 keys may begin
+        if (cut)
+          exps(kPkTile / 4, BoolConstant<false>{});
+        else
+          exps(kPkTile / 4, BoolConstant<true>{});
+        tmem_st32(s_row + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
         {
           const float2 s01 = f2_unpack(f2_add(rs4[0], rs4[1])), s23 = f2_unpack(f2_add(rs4[2], rs4[3]));
           l_run += (s01.x + s01.y) + (s23.x + s23.y);

@@ -57,6 +57,30 @@ __device__ __forceinline__ void zero_tile_rows(uint8_t* tile, int row0) {
   __syncwarp();
 }
 
+// A pair of 2^x on the FMA pipes, x from -125 up (below: 2^-125; NaN stays NaN): Cody-Waite
+// range reduction (W. J. Cody and W. Waite, "Software Manual for the Elementary Functions",
+// 1980) to f in [-1/2, 1/2], a degree-5 polynomial fitted for least largest relative error
+// there (7.5e-8), the integer part added to the exponent field.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long exp2_poly2(unsigned long long y) {
+  const float2 v = f2_unpack(y);
+  const unsigned long long x = f2_pack(max_nan(v.x, -125.0f), max_nan(v.y, -125.0f));
+  const unsigned long long t = f2_add(x, f2_splat(12582912.0f));  // 1.5 2^23: the low bits hold round(x)
+  const unsigned long long f = f2_fma(f2_add(t, f2_splat(-12582912.0f)), f2_splat(-1.0f), x);
+  unsigned long long q = f2_fma(f2_splat(0.0013276472454890609f), f, f2_splat(0.009675540961325169f));
+  q = f2_fma(q, f, f2_splat(0.05550713092088699f));
+  q = f2_fma(q, f, f2_splat(0.24022120237350464f));
+  q = f2_fma(q, f, f2_splat(0.6931469440460205f));
+  q = f2_fma(q, f, f2_splat(1.0000001192092896f));
+  const float2 n = f2_unpack(t), e = f2_unpack(q);
+  return f2_pack(__int_as_float(__float_as_int(e.x) + (__float_as_int(n.x) << 23)),
+                 __int_as_float(__float_as_int(e.y) + (__float_as_int(n.y) << 23)));
+}
+
 // tanh on the FMA pipes for |y| <= 1/2: an odd polynomial fitted for least largest error of
 // tanh(y)/y on that range (1.3e-8; 2^-24 absolute with its fp32 roundings).
 constexpr float kTanhPolyLimit = 0.5f;
