@@ -46,6 +46,7 @@ constexpr int kStages = 5;
 constexpr int kMaxCtas = 148;
 constexpr int kMinSplit = 8;         // a unit of more key tiles may be cut
 constexpr int kMinShare = 4;         // key tiles a CTA takes at least
+constexpr int kUnitCost = 2;         // see unit_weight
 constexpr float kRescaleLog2 = 8.0f;
 constexpr int kPolyEvery = 8;        // one pair of exponentials in this many runs on the FMA pipes
 constexpr size_t kSmem = 1024 + static_cast<size_t>(kPkTileBytes) * (2 + kStages) + 2048;
@@ -85,6 +86,10 @@ __device__ __forceinline__ int unit_tiles(const DocRows& d, const FwdParams& p, 
   return max(1, tiles_seen(d, p, u * 2 * p.per_tile, 2 * p.per_tile));
 }
 
+// A unit's weight in the shares: loading Q, the first scores and the output cost about as much
+// as two key tiles (texts of 1 to 4 tiles: without it some CTAs took three times the work).
+__device__ __forceinline__ int unit_weight(const DocRows& d, const FwdParams& p, int u) { return unit_tiles(d, p, u) + kUnitCost; }
+
 template <typename T>
 __device__ __forceinline__ T warp_incl_scan(T v) {
   const int lane = threadIdx.x & 31;
@@ -107,8 +112,8 @@ __device__ __forceinline__ int doc_waves(const DocRows& d, const FwdParams& p) {
 
 constexpr int kWaveDocs = 32;  // documents with waves (the first ones; more are shared out by key tiles)
 struct Share {
-  int64_t s, e;   // this CTA's key tiles of what the waves leave
-  int64_t total;  // all key tiles of it
+  int64_t s, e;   // this CTA's part of what the waves leave, in key tiles and unit costs
+  int64_t total;  // all of it
   int64_t at;     // first key tile of the unit below
   int ctas;       // CTAs that share it
   int doc, unit;
@@ -133,16 +138,16 @@ __device__ int64_t doc_left(const FwdParams& p, int d0, int& n_wave, int* list) 
     } else if (pairs > 0) {
       int64_t one = 0;
       if (p.a.causal_block == 0)
-        one = static_cast<int64_t>(pairs) * unit_tiles(doc, p, 0);
+        one = static_cast<int64_t>(pairs) * unit_weight(doc, p, 0);
       else
-        for (int u = 0; u < pairs; ++u) one += unit_tiles(doc, p, u);
+        for (int u = 0; u < pairs; ++u) one += unit_weight(doc, p, u);
       w = one * p.groups;
     }
   }
   const unsigned has = __ballot_sync(0xffffffffu, waves > 0);
   const int rank = n_wave + __popc(has & ((1u << lane) - 1u));
   if (waves > 0 && rank < kWaveDocs) {
-    w -= static_cast<int64_t>(waves) * p.ctas * unit_tiles(doc, p, 0);
+    w -= static_cast<int64_t>(waves) * p.ctas * unit_weight(doc, p, 0);
     if (list) list[rank] = d;
   }
   n_wave = min(n_wave + __popc(has), kWaveDocs);
@@ -151,7 +156,7 @@ __device__ int64_t doc_left(const FwdParams& p, int d0, int& n_wave, int* list) 
     const DocRows x = load_doc(p.a, d0 + src);
     const int n = doc_pairs(x, p);
     int64_t s = 0;
-    for (int u = lane; u < n; u += 32) s += unit_tiles(x, p, u);
+    for (int u = lane; u < n; u += 32) s += unit_weight(x, p, u);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == src) w = s * p.groups;
@@ -191,17 +196,17 @@ __device__ void find_share(const FwdParams& p, Share& out) {
   const DocRows doc = load_doc(p.a, doc_i);
   const int pairs = doc_pairs(doc, p);
   if (p.a.causal_block == 0) {
-    const int n = unit_tiles(doc, p, 0), k = static_cast<int>(left / n);
+    const int n = unit_weight(doc, p, 0), k = static_cast<int>(left / n);
     unit = k + (out.in_waves(doc_i) ? doc_waves(doc, p) * p.ctas : 0);
     at += static_cast<int64_t>(k) * n;
   } else {
     int64_t one = 0;
     for (int u0 = 0; u0 < pairs; u0 += 32)
-      one += __shfl_sync(0xffffffffu, warp_incl_scan(static_cast<int64_t>(u0 + lane < pairs ? unit_tiles(doc, p, u0 + lane) : 0)), 31);
+      one += __shfl_sync(0xffffffffu, warp_incl_scan(static_cast<int64_t>(u0 + lane < pairs ? unit_weight(doc, p, u0 + lane) : 0)), 31);
     const int group = static_cast<int>(left / one);
     left -= one * group, at += one * group;
     for (int u0 = 0;; u0 += 32) {
-      const int64_t w = u0 + lane < pairs ? unit_tiles(doc, p, u0 + lane) : 0, incl = warp_incl_scan(w);
+      const int64_t w = u0 + lane < pairs ? unit_weight(doc, p, u0 + lane) : 0, incl = warp_incl_scan(w);
       const int64_t sum = __shfl_sync(0xffffffffu, incl, 31);
       if (left >= sum) {
         left -= sum, at += sum;
@@ -230,14 +235,14 @@ struct Piece {
 // (where every one counts). Positions are relative to the share's first key tile.
 struct Walk {
   int wave_doc, wave;  // next wave
-  int at, end, n;      // unit's first key tile, the share's end, the unit's key tiles (0: none yet)
+  int at, end, weight;  // unit's first key tile, the share's end, the unit's weight (0: none yet)
   int doc, unit;
   DocRows d;           // document of the piece
   Piece x;
 };
 __device__ __forceinline__ void walk_begin(Walk& w, const Share& s) {
   w.wave_doc = w.wave = 0;
-  w.end = static_cast<int>(s.e - s.s), w.n = 0;
+  w.end = static_cast<int>(s.e - s.s), w.weight = 0;
   w.at = w.end > 0 ? static_cast<int>(s.at - s.s) : 0;
   w.doc = s.doc, w.unit = s.unit - 1;
 }
@@ -269,17 +274,18 @@ __device__ __forceinline__ bool walk_step(Walk& w, const FwdParams& p, const Sha
       return true;
     }
   }
-  int at = w.at, n = w.n, unit = w.unit;
-  if (at + n >= w.end) return false;
+  int at = w.at, weight = w.weight, unit = w.unit;
+  if (at + weight >= w.end) return false;
   DocRows d = load_doc(p.a, w.doc);
-  while (at + n < w.end) {
-    at += n;
+  while (at + weight < w.end) {
+    at += weight;
     ++unit;
     while (unit >= doc_pairs(d, p) * p.groups) {
       d = load_doc(p.a, ++w.doc);
       unit = s.in_waves(w.doc) ? doc_waves(d, p) * p.ctas : 0;
     }
-    n = unit_tiles(d, p, unit % doc_pairs(d, p));
+    const int n = unit_tiles(d, p, unit % doc_pairs(d, p));
+    weight = n + kUnitCost;  // the cost lies behind the key tiles
     const bool may_cut = p.may_split && n > kMinSplit;
     int a = 0, b = n;
     bool mine = at >= 0;
@@ -292,10 +298,10 @@ __device__ __forceinline__ bool walk_step(Walk& w, const FwdParams& p, const Sha
     make_piece(w.x, d, p, unit, a, b, n);
     w.x.slot = 2 * static_cast<int>(blockIdx.x) + (at <= 0 ? 0 : 1);  // the share's first piece, or its last
     w.x.unit_end = at + n;
-    w.at = at, w.n = n, w.unit = unit, w.d = d;
+    w.at = at, w.weight = weight, w.unit = unit, w.d = d;
     return true;
   }
-  w.at = at, w.n = n;
+  w.at = at, w.weight = weight;
   return false;
 }
 // The same for a whole warp.
@@ -327,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* kv_empty = kv_full + kStages;
   uint64_t* s_full = kv_empty + kStages;     // [2]
   uint64_t* p_full = s_full + 2;             // [2]
-  uint64_t* p_half = p_full + 2;             // [2]: its first 64 columns
+  uint64_t* p_half = p_full + 2;             // [2]: its first 96 columns
   uint64_t* o_final = p_half + 2;            // [2]
   uint64_t* ragged = o_final + 2;            // a ragged V tile has landed; its end is cleared
   uint64_t* cleared = ragged + 1;
@@ -451,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           if (elect_lane()) {
 #pragma unroll
-            for (int k = 4 * h; k < 4 * h + 4; ++k)
+            for (int k = 6 * h; k < 6 + 2 * h; ++k)
               tc_mma_bf16_ts(tm + 256 + t * kPkTile, tm + t * kPkTile + k * 8, vd + ((k * 16 * 128) >> 4), idesc_pv,
                              (!first || k > 0) ? 1u : 0u);
           }
@@ -608,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Masked entries are exactly 0 (the polynomial stops at 2^-125), so it is left out there.
         auto exps = [&](int c0, auto poly) {
 #pragma unroll
-          for (int c = c0; c < c0 + kPkTile / 4; ++c) {
+          for (int c = c0; c < (c0 ? 64 : 48); ++c) {
             const unsigned long long y2 = f2_fma(f2_pack(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])), mult2, nb2);
             float2 e;
             if (poly.value && c % kPolyEvery == kPolyEvery - 1) {
@@ -626,6 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           exps(0, BoolConstant<true>{});
         tmem_st32(s_row, *reinterpret_cast<uint32_t(*)[32]>(r));
+        tmem_st16(s_row + 32, *reinterpret_cast<uint32_t(*)[16]>(r + 32));
         if (rescale) {
           // S_t(j) ready implies that PV_t(j-1) completed, and PV_t(j) waits for this
           // thread's arrival below: O_t is current and idle here.
@@ -642,12 +649,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&p_half[t]);  // the product over the first 64 keys may begin
+        mbar_arrive(&p_half[t]);  // the product over the first 96 keys may begin
         if (cut)
-          exps(kPkTile / 4, BoolConstant<false>{});
+          exps(48, BoolConstant<false>{});
         else
-          exps(kPkTile / 4, BoolConstant<true>{});
-        tmem_st32(s_row + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
+          exps(48, BoolConstant<true>{});
+        tmem_st16(s_row + 48, *reinterpret_cast<uint32_t(*)[16]>(r + 48));
         {
           const float2 s01 = f2_unpack(f2_add(rs4[0], rs4[1])), s23 = f2_unpack(f2_add(rs4[2], rs4[3]));
           l_run += (s01.x + s01.y) + (s23.x + s23.y);
@@ -810,8 +817,8 @@ int launch_attn_packed_tc(const PackedAttn& a, void* ws, size_t ws_bytes, cudaSt
   p.ctas = device_sms() < kMaxCtas ? device_sms() : kMaxCtas;
   const SplitLayout l = split_layout(a);
   p.slot_rows = l.slot_rows;
-  if (ws) {
-    if (ws_bytes < l.total) return WAN_ERR_WORKSPACE;
+  if (ws && ws_bytes < l.total) return WAN_ERR_WORKSPACE;
+  if (ws && a.k_rows > kMinSplit * kPkTile) {  // no unit of fewer keys is cut
     uint8_t* w = static_cast<uint8_t*>(ws);
     p.part_o = reinterpret_cast<float*>(w);
     p.part_ml = reinterpret_cast<float2*>(w + l.o_bytes);
