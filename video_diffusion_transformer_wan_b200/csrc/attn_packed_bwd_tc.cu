@@ -17,8 +17,11 @@
 //        forms S(j+1), and dP(j+1) as soon as dP(j) is read; ds goes back over S(j) in bf16
 //        (each half into its own columns) as the A operand of dQ += ds K_j.
 //   dkv: the transposed scores, S^T = K Q^T and dP^T = V dO^T, so that p^T and ds^T are A
-//        operands too; both go back over S^T. TMEM holds S^T, dP^T, dV and dK: dP^T(i+1)
-//        overlaps the score warps, S^T(i+1) follows the products of tile i.
+//        operands too; both go back over S^T. Query tiles have 64 rows, so that TMEM holds
+//        S^T and dP^T twice beside dV and dK: while the score warps work on tile i the tensor
+//        core forms tile i+1's scores and tile i-1's products, and four tiles are on their
+//        way. (With 128 rows, held once, it waited for loads and scores in turn: 697 us
+//        against 465 us on 9,371 rows of 12 heads.)
 // Rows behind a document's end belong to others: where they are summed over (K rows in dq; Q
 // and dO rows in dkv) they are cleared in shared memory, elsewhere masked or not stored.
 #include <math.h>
@@ -34,11 +37,15 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kScoreThreads = 256;
 constexpr int kDqStages = 5;
-constexpr int kDkvStages = 4;
+constexpr int kDkvStages = 4;                // query tiles of 64 rows on their way
+constexpr int kHalfSpan = 64 * 128;          // 64 rows of one 128-byte swizzled span
+constexpr int kHalfBytes = 2 * kHalfSpan;    // 64 rows of 128 dims
 constexpr size_t kDqSmem = 1024 + static_cast<size_t>(kPkTileBytes) * (2 + kDqStages) + 512;
-// per staged query tile: float2 (log-sum, delta) or, with distances, float4 and a key count
-constexpr int kStatBytes = kPkTile * (16 + 4);
-constexpr size_t kDkvSmem = 1024 + static_cast<size_t>(kPkTileBytes) * (2 + kDkvStages) + 2 * kStatBytes + 512;
+// per staged query: float2 (log-sum, delta) or, with distances, float4; and a key count
+constexpr int kStatBytes = 64 * (16 + 4);
+constexpr int kStatBufs = 4;
+constexpr size_t kDkvSmem =
+    1024 + 2 * static_cast<size_t>(kPkTileBytes) + 2 * static_cast<size_t>(kHalfBytes) * kDkvStages + kStatBufs * kStatBytes + 512;
 static_assert(kDqSmem <= 232448 && kDkvSmem <= 232448, "shared memory of an SM");
 
 struct BwdParams {
@@ -301,8 +308,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Query tiles of a document that see key tile `key0`, over the head groups of one key head:
-// tile i of the walk is query tile first_tile + i % per_group of group i / per_group.
+// Query tiles (64 packed rows) of a document that see key tile `key0`, over the head groups of
+// one key head: tile i of the walk is query tile first_tile + i % per_group of group
+// i / per_group.
 struct QueryWalk {
   int first_tile, per_group, n;
 };
@@ -321,22 +329,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sKV = smem;                      // K, then V
-  uint8_t* sQ = sKV + 2 * kPkTileBytes;     // [kDkvStages]: Q_0, dO_0, Q_1, dO_1, ...
-  uint8_t* stats = sQ + kDkvStages * kPkTileBytes;  // [2] per query: -log-sum, -delta (, slope, position), then keys seen
-  uint64_t* bars = reinterpret_cast<uint64_t*>(stats + 2 * kStatBytes);
+  uint8_t* sQ = sKV + 2 * kPkTileBytes;     // [kDkvStages]: Q_i (64 rows), dO_i
+  uint8_t* stats = sQ + kDkvStages * 2 * kHalfBytes;  // [kStatBufs] per query: -log-sum, -delta (, slope, position), then keys seen
+  uint64_t* bars = reinterpret_cast<uint64_t*>(stats + kStatBufs * kStatBytes);
   uint64_t* kv_full = bars;
   uint64_t* q_full = bars + 1;
   uint64_t* q_empty = q_full + kDkvStages;
-  uint64_t* s_full = q_empty + kDkvStages;
-  uint64_t* y_free = s_full + 1;
-  uint64_t* p_full = s_full + 2;            // p^T and ds^T are in place
-  uint64_t* done = s_full + 3;
-  uint64_t* ragged = s_full + 4;
-  uint64_t* cleared = s_full + 5;
-  uint64_t* st_full = s_full + 6;           // [2]
-  uint64_t* st_empty = s_full + 8;          // [2]
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(s_full + 10);
-  int* found = reinterpret_cast<int*>(s_full + 11);
+  uint64_t* s_full = q_empty + kDkvStages;  // [2] S^T(i) and dP^T(i) are there (i & 1)
+  uint64_t* p_full = s_full + 2;            // [2] p^T and ds^T are in place
+  uint64_t* done = s_full + 4;
+  uint64_t* ragged = s_full + 5;
+  uint64_t* cleared = s_full + 6;
+  uint64_t* st_full = s_full + 7;           // [kStatBufs]
+  uint64_t* st_empty = st_full + kStatBufs;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(st_empty + kStatBufs);
+  int* found = reinterpret_cast<int*>(st_empty + kStatBufs + 1);
 
   int di, tile;
   if (!cta_tile(p.a.cu_k, p.a.n_docs, p.a.k_rows, kPkTile, found, di, tile)) return;
@@ -349,17 +356,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
     for (int s = 0; s < kDkvStages; ++s) mbar_init(&q_full[s], 1), mbar_init(&q_empty[s], 1);
-    mbar_init(s_full, 1);
-    mbar_init(y_free, kScoreThreads);
-    mbar_init(p_full, kScoreThreads);
+    for (int b = 0; b < 2; ++b) mbar_init(&s_full[b], 1), mbar_init(&p_full[b], kScoreThreads);
     mbar_init(done, 1);
     mbar_init(ragged, 1);
     mbar_init(cleared, 1);
-    for (int b = 0; b < 2; ++b) mbar_init(&st_full[b], 1), mbar_init(&st_empty[b], kScoreThreads);
+    for (int b = 0; b < kStatBufs; ++b) mbar_init(&st_full[b], 1), mbar_init(&st_empty[b], kScoreThreads);
     fence_mbar_init();
   }
   // Rows that no copy writes take part in the sums over queries.
-  if (used < kPkTile && warp >= 4 && warp < 4 + kDkvStages) zero_tile_rows(sQ + (warp - 4) * kPkTileBytes, used);
+  if (used < 64 && warp >= 4 && warp < 4 + 2 * kDkvStages) zero_tile_rows<64>(sQ + (warp - 4) * kHalfBytes, used);
   if (warp == 1) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
@@ -367,7 +372,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_holder, Y = tmem + 128, dV = tmem + 256, dK = tmem + 384;
+  // S^T(i) at 64 (i & 1), dP^T(i) 128 columns on
+  const uint32_t tmem = *tmem_holder, dV = tmem + 256, dK = tmem + 384;
   const int hk = blockIdx.y, group0 = hk * (p.a.H / p.a.Hk / p.pack);
 
   if (warp == 0) {
@@ -377,149 +383,185 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_load_2d(sKV + c * kPkSpan, &mapK, kv_full, hk * kPkD + 64 * c, doc.k0 + key0);
         tma_load_2d(sKV + kPkTileBytes + c * kPkSpan, &mapV, kv_full, hk * kPkD + 64 * c, doc.k0 + key0);
       }
-      int issued = 0;
-      for (; issued < 2 * w.n; ++issued) {
-        const int stage = issued % kDkvStages, i = issued >> 1, g = i / w.per_group;
-        if (!mbar_wait(&q_empty[stage], static_cast<uint32_t>((issued / kDkvStages) & 1) ^ 1u, p.err)) break;
-        mbar_arrive_expect_tx(&q_full[stage], static_cast<uint32_t>(used) * 256u);
-        for (int c = 0; c < 2; ++c)
-          tma_load_3d(sQ + stage * kPkTileBytes + c * kPkSpan, issued & 1 ? &mapO : &mapQ, &q_full[stage], 64 * c,
-                      (group0 + g) * p.pack, doc.q0 + (w.first_tile + i - g * w.per_group) * p.per_tile);
+      int i = 0;
+      for (; i < w.n; ++i) {
+        const int stage = i % kDkvStages, g = i / w.per_group;
+        if (!mbar_wait(&q_empty[stage], static_cast<uint32_t>((i / kDkvStages) & 1) ^ 1u, p.err)) break;
+        mbar_arrive_expect_tx(&q_full[stage], 2 * static_cast<uint32_t>(used) * 256u);
+        uint8_t* at = sQ + stage * 2 * kHalfBytes;
+        const int y = (group0 + g) * p.pack, z = doc.q0 + (w.first_tile + i - g * w.per_group) * p.per_tile;
+        for (int c = 0; c < 2; ++c) {
+          tma_load_3d(at + c * kHalfSpan, &mapQ, &q_full[stage], 64 * c, y, z);
+          tma_load_3d(at + kHalfBytes + c * kHalfSpan, &mapO, &q_full[stage], 64 * c, y, z);
+        }
       }
       mbar_wait(kv_full, 0, p.err);  // every copy this thread started has landed before it leaves
       for (int s = 0; s < kDkvStages; ++s) {
-        const int m = issued / kDkvStages + (s < issued % kDkvStages ? 1 : 0);
+        const int m = i / kDkvStages + (s < i % kDkvStages ? 1 : 0);
         if (m > 0) mbar_wait(&q_full[s], static_cast<uint32_t>((m - 1) & 1), p.err);
       }
     }
   } else if (warp == 1) {
     const int nu = uniform(w.n), per_group = uniform(w.per_group);
     if (nu > 0) {
-      const uint32_t id_kk = idesc_bf16_f32(kPkTile, kPkTile, 0, 0), id_mn = idesc_bf16_f32(kPkTile, kPkD, 0, 1);
+      const uint32_t id_kk = idesc_bf16_f32(kPkTile, 64, 0, 0), id_mn = idesc_bf16_f32(kPkTile, kPkD, 0, 1);
       const uint32_t tm = uniform(tmem);
       const uint64_t k_desc = sdesc_sw128(smem_u32(sKV), 16, 1024), v_desc = sdesc_sw128(smem_u32(sKV + kPkTileBytes), 16, 1024);
-      const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024), qt_desc = sdesc_sw128(smem_u32(sQ), kPkSpan, 1024);
-      auto stage_off = [](int pos) { return static_cast<uint32_t>((pos % kDkvStages * kPkTileBytes) >> 4); };
-      auto wait_pos = [&](int pos) {
-        return mbar_wait_warp(&q_full[pos % kDkvStages], static_cast<uint32_t>((pos / kDkvStages) & 1), p.err);
-      };
+      const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024), qt_desc = sdesc_sw128(smem_u32(sQ), kHalfSpan, 1024);
       int ragged_seen = 0;
       const bool ragged_end = uniform(last_rows) < used;
-      // Tile i is there, its rows behind the document's end cleared.
-      auto arrived = [&](int i) {
-        if (!wait_pos(2 * i) || !wait_pos(2 * i + 1)) return false;
+      // S^T(i) = K Q_i^T and dP^T(i) = V dO_i^T, once the tile is there and its rows behind the
+      // document's end are cleared.
+      auto scores = [&](int i) {
+        const int stage = i % kDkvStages;
+        if (!mbar_wait_warp(&q_full[stage], static_cast<uint32_t>((i / kDkvStages) & 1), p.err)) return false;
         if (ragged_end && (i + 1) % per_group == 0) {
           if (lane == 0) mbar_arrive(ragged);
           if (!mbar_wait_warp(cleared, static_cast<uint32_t>(ragged_seen++ & 1), p.err)) return false;
         }
+        const uint64_t qd = q_desc + static_cast<uint32_t>((stage * 2 * kHalfBytes) >> 4);
+        const uint64_t od = qd + (kHalfBytes >> 4);
+        const uint32_t to = tm + 64 * (i & 1);
+        if (elect_lane()) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            tc_mma_bf16(to, k_desc + (((k >> 2) * kPkSpan + (k & 3) * 32) >> 4), qd + (((k >> 2) * kHalfSpan + (k & 3) * 32) >> 4),
+                        id_kk, k > 0 ? 1u : 0u);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            tc_mma_bf16(to + 128, v_desc + (((k >> 2) * kPkSpan + (k & 3) * 32) >> 4),
+                        od + (((k >> 2) * kHalfSpan + (k & 3) * 32) >> 4), id_kk, k > 0 ? 1u : 0u);
+          tc_commit(&s_full[i & 1]);
+        }
         return true;
       };
-      bool ok = mbar_wait_warp(kv_full, 0, p.err) && arrived(0);
-      if (ok && elect_lane()) {
-        mma_ss(tm, k_desc, q_desc, id_kk);
-        mma_ss(tm + 128, v_desc, q_desc + stage_off(1), id_kk);
-        tc_commit(s_full);
-      }
+      bool ok = mbar_wait_warp(kv_full, 0, p.err) && scores(0);
+      if (ok && nu > 1) ok = scores(1);
       for (int i = 0; ok && i < nu; ++i) {
-        const bool more = i + 1 < nu;
-        if (more) {
-          if (!arrived(i + 1) || !mbar_wait_warp(y_free, static_cast<uint32_t>(i & 1), p.err)) break;
-          tc_fence_after();
-          const uint64_t od = q_desc + stage_off(2 * i + 3);
-          if (elect_lane()) mma_ss(tm + 128, v_desc, od, id_kk);
-        }
-        if (!mbar_wait_warp(p_full, static_cast<uint32_t>(i & 1), p.err)) break;
+        if (!mbar_wait_warp(&p_full[i & 1], static_cast<uint32_t>((i >> 1) & 1), p.err)) break;
         tc_fence_after();
-        const uint64_t od = qt_desc + stage_off(2 * i + 1), qd = qt_desc + stage_off(2 * i), next = q_desc + stage_off(2 * i + 2);
+        const int stage = i % kDkvStages;
+        const uint64_t qd = qt_desc + static_cast<uint32_t>((stage * 2 * kHalfBytes) >> 4), od = qd + (kHalfBytes >> 4);
+        const uint32_t from = tm + 64 * (i & 1);
         if (elect_lane()) {
-          mma_ts_halves(tm + 256, tm, od, id_mn, i == 0);
-          tc_commit(&q_empty[(2 * i + 1) % kDkvStages]);
-          mma_ts_halves(tm + 384, tm + 32, qd, id_mn, i == 0);
-          tc_commit(&q_empty[2 * i % kDkvStages]);
-          if (more) {
-            mma_ss(tm, k_desc, next, id_kk);
-            tc_commit(s_full);
-          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc_mma_bf16_ts(tm + 256, from + (k >> 1) * 32 + (k & 1) * 8, od + ((k * 16 * 128) >> 4), id_mn, (i > 0 || k > 0) ? 1u : 0u);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc_mma_bf16_ts(tm + 384, from + 16 + (k >> 1) * 32 + (k & 1) * 8, qd + ((k * 16 * 128) >> 4), id_mn,
+                           (i > 0 || k > 0) ? 1u : 0u);
+          tc_commit(&q_empty[stage]);
         }
+        if (i + 2 < nu) ok = scores(i + 2);
       }
       if (elect_lane()) tc_commit(done);
       mbar_wait_warp(done, 0, p.err);
     }
   } else if (warp == 2) {
     // The numbers of each query tile's columns. A column of no query, and a query that sees
-    // nothing, get p = 2^(s - infinity) = 0.
-    for (int i = 0; i < w.n; ++i) {
-      const int b = i & 1, g = i / w.per_group;
-      if (i >= 2 && !mbar_wait_warp(&st_empty[b], static_cast<uint32_t>(((i >> 1) - 1) & 1), p.err)) break;
-      uint8_t* st = stats + b * kStatBytes;
+    // nothing, get p = 2^(s - infinity) = 0. Four tiles' loads are in flight (with one, this
+    // warp held up all others: 786 us against 465).
+    float lse[kStatBufs][2], delta[kStatBufs][2];
+    int place[2], in_tile[2];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int m = c * 32 + lane, qi = m / p.pack, head = (group0 + g) * p.pack + m - qi * p.pack;
-        const int q = (w.first_tile + i - g * w.per_group) * p.per_tile + qi;
-        const bool live = qi < p.per_tile && q < doc.Lq;
-        float nl = -INFINITY, nd = 0.f, slope2 = 0.f;
-        int seen = 0;
-        if (live) {
-          const int64_t stat = static_cast<int64_t>(head) * p.a.q_rows + doc.q0 + q;
-          const float lse = p.a.lse[stat];
-          if (lse != -INFINITY) nl = -lse * kLog2e, nd = -p.a.delta[stat];
-          seen = seen_keys(q, doc.off, doc.Lk, doc.prefix, p.a.causal_block);
-          if (!kPlain && p.a.slopes) slope2 = __ldg(p.a.slopes + head) * kLog2e;
+    for (int c = 0; c < 2; ++c) {
+      const int m = c * 32 + lane;
+      in_tile[c] = m / p.pack;
+      place[c] = m - in_tile[c] * p.pack;
+      if (in_tile[c] >= p.per_tile) in_tile[c] = 1 << 30;  // no query
+    }
+    int fetch_tile = 0, fetch_group = 0;  // the next tile to fetch
+    auto fetch = [&](float (&l)[2], float (&d)[2]) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int64_t q = static_cast<int64_t>(w.first_tile + fetch_tile) * p.per_tile + in_tile[c];
+        l[c] = -INFINITY, d[c] = 0.f;
+        if (q < doc.Lq) {
+          const int64_t stat = static_cast<int64_t>((group0 + fetch_group) * p.pack + place[c]) * p.a.q_rows + doc.q0 + q;
+          l[c] = p.a.lse[stat], d[c] = p.a.delta[stat];
         }
-        if (kPlain)
-          reinterpret_cast<float2*>(st)[m] = make_float2(nl, nd);
-        else
-          reinterpret_cast<float4*>(st)[m] = make_float4(nl, nd, slope2, static_cast<float>(q + doc.off - key0));
-        reinterpret_cast<int*>(st + kPkTile * 16)[m] = seen;
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&st_full[b]);
+      if (++fetch_tile == w.per_group) fetch_tile = 0, ++fetch_group;
+    };
+#pragma unroll
+    for (int u = 0; u < kStatBufs; ++u)
+      if (u < w.n) fetch(lse[u], delta[u]);
+    int tile_i = 0, group_i = 0;
+    bool ok = true;
+    for (int i0 = 0; ok && i0 < w.n; i0 += kStatBufs) {
+#pragma unroll
+      for (int u = 0; u < kStatBufs; ++u) {
+        const int i = i0 + u;
+        if (!ok || i >= w.n) continue;
+        uint8_t* st = stats + u * kStatBytes;
+        if (i0 > 0 && !mbar_wait_warp(&st_empty[u], static_cast<uint32_t>((i0 / kStatBufs - 1) & 1), p.err)) {
+          ok = false;
+          continue;
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int m = c * 32 + lane;
+          const int64_t q = static_cast<int64_t>(w.first_tile + tile_i) * p.per_tile + in_tile[c];
+          const bool there = q < doc.Lq, sees = lse[u][c] != -INFINITY;
+          const float nl = sees ? -lse[u][c] * kLog2e : -INFINITY, nd = sees ? -delta[u][c] : 0.f;
+          if (kPlain) {
+            reinterpret_cast<float2*>(st)[m] = make_float2(nl, nd);
+          } else {
+            const float slope2 = p.a.slopes && there ? __ldg(p.a.slopes + (group0 + group_i) * p.pack + place[c]) * kLog2e : 0.f;
+            reinterpret_cast<float4*>(st)[m] =
+                make_float4(nl, nd, slope2, there ? static_cast<float>(static_cast<int>(q) + doc.off - key0) : 0.f);
+          }
+          reinterpret_cast<int*>(st + 64 * 16)[m] =
+              there ? seen_keys(static_cast<int>(q), doc.off, doc.Lk, doc.prefix, p.a.causal_block) : 0;
+        }
+        if (++tile_i == w.per_group) tile_i = 0, ++group_i;
+        if (i + kStatBufs < w.n) fetch(lse[u], delta[u]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&st_full[u]);
+      }
     }
   } else if (warp == 3) {
     if (last_rows < used) {
       int k = 0;
       for (int i = w.per_group - 1; w.per_group > 0 && i < w.n; i += w.per_group, ++k) {
         if (!mbar_wait_warp(ragged, static_cast<uint32_t>(k & 1), p.err)) break;
-        zero_tile_rows(sQ + 2 * i % kDkvStages * kPkTileBytes, last_rows);
-        zero_tile_rows(sQ + (2 * i + 1) % kDkvStages * kPkTileBytes, last_rows);
+        zero_tile_rows<64>(sQ + i % kDkvStages * 2 * kHalfBytes, last_rows);
+        zero_tile_rows<64>(sQ + i % kDkvStages * 2 * kHalfBytes + kHalfBytes, last_rows);
         if (lane == 0) mbar_arrive(cleared);
       }
     }
   } else {
     const int half = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
-    const uint32_t at = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t x = tmem + at + 64 * half;
+    const uint32_t at = (static_cast<uint32_t>((warp & 3) * 32) << 16) + 32 * half;
     const bool live = row < keys;
     bool ok = true;
     for (int i = 0; i < w.n; ++i) {
-      const int b = i & 1;
-      if (!mbar_wait_warp(&st_full[b], static_cast<uint32_t>((i >> 1) & 1), p.err) ||
-          !mbar_wait_warp(s_full, static_cast<uint32_t>(i & 1), p.err)) {
+      const int b = i % kStatBufs;
+      if (!mbar_wait_warp(&st_full[b], static_cast<uint32_t>((i / kStatBufs) & 1), p.err) ||
+          !mbar_wait_warp(&s_full[i & 1], static_cast<uint32_t>((i >> 1) & 1), p.err)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      uint32_t s[64], g[64];
-      tmem_ld32(x, *reinterpret_cast<uint32_t(*)[32]>(s));
-      tmem_ld32(x + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
-      tmem_ld32(Y + at + 64 * half, *reinterpret_cast<uint32_t(*)[32]>(g));
-      tmem_ld32(Y + at + 64 * half + 32, *reinterpret_cast<uint32_t(*)[32]>(g + 32));
+      const uint32_t x = tmem + 64 * (i & 1) + at;
+      uint32_t s[32], g[32];
+      tmem_ld32(x, s);
+      tmem_ld32(x + 128, g);
       tmem_ld_wait();
-      tc_fence_before();
-      mbar_arrive(y_free);
       const uint8_t* st = stats + b * kStatBytes;
       if (!kPlain && p.a.cap > 0.f) cap_scores(s, p.cap_in, live);
       const unsigned long long mult2 = f2_splat(p.mult);
       const float key = static_cast<float>(row);
 #pragma unroll
-      for (int c = 0; c < 64; c += 2) {
+      for (int c = 0; c < 32; c += 2) {
         float2 nl, nd;
         const unsigned long long t = f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
         if constexpr (kPlain) {
-          const float4 v = reinterpret_cast<const float4*>(st)[32 * half + (c >> 1)];
+          const float4 v = reinterpret_cast<const float4*>(st)[16 * half + (c >> 1)];
           nl = make_float2(v.x, v.z), nd = make_float2(v.y, v.w);
         } else {
-          const float4 v0 = reinterpret_cast<const float4*>(st)[64 * half + c], v1 = reinterpret_cast<const float4*>(st)[64 * half + c + 1];
+          const float4 v0 = reinterpret_cast<const float4*>(st)[32 * half + c], v1 = reinterpret_cast<const float4*>(st)[32 * half + c + 1];
           nl = make_float2(v0.x - v0.z * fabsf(v0.w - key), v1.x - v1.z * fabsf(v1.w - key)), nd = make_float2(v0.y, v1.y);
         }
         const float2 e = f2_unpack(f2_fma(t, mult2, f2_pack(nl.x, nl.y)));
@@ -532,35 +574,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (p.a.causal_block > 0) {
         // queries see ever more keys: the tile's first column decides whether any is masked
-        const int* seen = reinterpret_cast<const int*>(st + kPkTile * 16);
+        const int* seen = reinterpret_cast<const int*>(st + 64 * 16);
         if (seen[0] < key0 + keys) {
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (key0 + row >= seen[64 * half + c]) s[c] = 0u, g[c] = 0u;
+          for (int c = 0; c < 32; ++c)
+            if (key0 + row >= seen[32 * half + c]) s[c] = 0u, g[c] = 0u;
         }
       }
       mbar_arrive(&st_empty[b]);
+      uint32_t out[32];  // p^T, then ds^T, over this half of S^T
 #pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        s[c] = pack_bf16x2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
-        g[c] = pack_bf16x2(__uint_as_float(g[2 * c]), __uint_as_float(g[2 * c + 1]));
+      for (int c = 0; c < 16; ++c) {
+        out[c] = pack_bf16x2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
+        out[16 + c] = pack_bf16x2(__uint_as_float(g[2 * c]), __uint_as_float(g[2 * c + 1]));
       }
-      tmem_st32(x, *reinterpret_cast<uint32_t(*)[32]>(s));
-      tmem_st32(x + 32, *reinterpret_cast<uint32_t(*)[32]>(g));
+      tmem_st32(x, out);
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(p_full);
+      mbar_arrive(&p_full[i & 1]);
     }
     if (ok && w.n > 0) ok = mbar_wait_warp(done, 0, p.err);
     if (ok) {
       tc_fence_after();
+      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const int64_t key_row = static_cast<int64_t>(doc.k0) + key0 + row;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {  // two quarters of dV, two of dK
         uint32_t r[32];
         const int col = 64 * half + 32 * (c & 1);
         if (w.n > 0) {
-          tmem_ld32((c < 2 ? dV : dK) + at + col, r);
+          tmem_ld32((c < 2 ? dV : dK) + lanes + col, r);
           tmem_ld_wait();
         } else {
 #pragma unroll
@@ -611,16 +654,22 @@ int launch_attn_packed_tc_bwd(const PackedAttn& a, cudaStream_t s) {
     for (auto kernel : {packed_dkv_tc_kernel<true>, packed_dkv_tc_kernel<false>})
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kDkvSmem));
   });
-  CUtensorMap mq, mo, mk, mv;
+  BwdParams p2 = p;  // the keys' kernel: query tiles of 64 rows
+  p2.pack = packed_heads_per_tile(a.H, a.Hk, 64);
+  p2.per_tile = 64 / p2.pack;
+  p2.groups = a.H / p2.pack;
+  CUtensorMap mq, mo, mk, mv, mq2, mo2;
   // without queries (or keys) none is loaded: any valid map will do
   const bool qs = a.q_rows > 0, ks = a.k_rows > 0;
   if (!make_packed_kv_map(&mk, ks ? a.k : a.q, ks ? a.k_stride : a.q_stride, ks ? a.k_rows : 1, a.Hk) ||
       !make_packed_kv_map(&mv, ks ? a.v : a.q, ks ? a.v_stride : a.q_stride, ks ? a.k_rows : 1, a.Hk))
     return WAN_ERR_CUDA;
   if (!qs) {
-    mq = mo = mk;
+    mq = mo = mq2 = mo2 = mk;
   } else if (!make_packed_q_map(&mq, a.q, a.q_stride, a.q_rows, a.H, p.pack) ||
-             !make_packed_q_map(&mo, a.d_o, a.do_stride, a.q_rows, a.H, p.pack)) {
+             !make_packed_q_map(&mo, a.d_o, a.do_stride, a.q_rows, a.H, p.pack) ||
+             !make_packed_q_map(&mq2, a.q, a.q_stride, a.q_rows, a.H, p2.pack, 64) ||
+             !make_packed_q_map(&mo2, a.d_o, a.do_stride, a.q_rows, a.H, p2.pack, 64)) {
     return WAN_ERR_CUDA;
   }
   const bool plain = a.cap == 0.f && !a.slopes;
@@ -634,7 +683,7 @@ int launch_attn_packed_tc_bwd(const PackedAttn& a, cudaStream_t s) {
   }
   if (ks) {
     const dim3 grid(static_cast<unsigned>(a.k_rows / kPkTile + a.n_docs), static_cast<unsigned>(a.Hk));
-    (plain ? packed_dkv_tc_kernel<true> : packed_dkv_tc_kernel<false>)<<<grid, kThreads, kDkvSmem, s>>>(mq, mo, mk, mv, p);
+    (plain ? packed_dkv_tc_kernel<true> : packed_dkv_tc_kernel<false>)<<<grid, kThreads, kDkvSmem, s>>>(mq2, mo2, mk, mv, p2);
     count_launches(1);
     return check_launch();
   }

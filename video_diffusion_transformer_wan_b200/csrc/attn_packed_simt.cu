@@ -342,23 +342,34 @@ __global__ void __launch_bounds__(kThreads) packed_dkv_kernel(const PackedAttn p
   store_rows<D>(p.dv, p.dv_stride, static_cast<int64_t>(doc.k0) + j0, keys, hk * p.d, p.d, gv, one);
 }
 
-// delta[h, row] = sum(do * o) of bf16 rows (for the tensor-core gradient), one warp per (row, head).
+// delta[h, row] = sum(do * o) of bf16 rows of 128 dims (for the tensor-core gradient): 16 lanes
+// a (row, head), four of them at a time.
 __global__ void __launch_bounds__(256) packed_delta_kernel(const PackedAttn p) {
-  const int64_t w = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = w / p.H;
-  const int h = static_cast<int>(w - row * p.H);
-  if (row >= p.q_rows) return;
-  const __nv_bfloat16* a = static_cast<const __nv_bfloat16*>(p.d_o) + row * p.do_stride + h * p.d;
-  const __nv_bfloat16* b = static_cast<const __nv_bfloat16*>(p.o) + row * p.o_stride + h * p.d;
-  float s = 0.f;
-  for (int c = 4 * lane; c < p.d; c += 128) {
-    const uint2 x = *reinterpret_cast<const uint2*>(a + c), y = *reinterpret_cast<const uint2*>(b + c);
-    s = fmaf(bf16_lo(x.x), bf16_lo(y.x), fmaf(bf16_hi(x.x), bf16_hi(y.x), fmaf(bf16_lo(x.y), bf16_lo(y.y), fmaf(bf16_hi(x.y), bf16_hi(y.y), s))));
+  const int lane = threadIdx.x & 15;
+  const int64_t all = static_cast<int64_t>(p.q_rows) * p.H, first = (static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4)) * 4;
+  uint4 x[4], y[4];
+  int64_t row[4];
+  int h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t w = first + i < all ? first + i : all - 1;
+    row[i] = w / p.H, h[i] = static_cast<int>(w - row[i] * p.H);
+    x[i] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.d_o) + row[i] * p.do_stride + h[i] * 128) + lane);
+    y[i] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.o) + row[i] * p.o_stride + h[i] * 128) + lane);
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (lane == 0) p.delta[static_cast<int64_t>(h) * p.q_rows + row] = s;
+  for (int i = 0; i < 4; ++i) {
+    float a[8], b[8], s = 0.f;
+    Raw8<__nv_bfloat16> r;
+    r.u = x[i];
+    unpack8(r, a);
+    r.u = y[i];
+    unpack8(r, b);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) s = fmaf(a[c], b[c], s);
+    s = sum16(s);
+    if (lane == 0 && first + i < all) p.delta[static_cast<int64_t>(h[i]) * p.q_rows + row[i]] = s;
+  }
 }
 
 // At most this many tiles: every document adds less than one partial tile.
@@ -399,8 +410,8 @@ int delta(const PackedAttn& p, cudaStream_t s) {
     count_launches(-1);
     return WAN_OK;
   }
-  const int64_t warps = static_cast<int64_t>(p.q_rows) * p.H;
-  packed_delta_kernel<<<static_cast<unsigned>((warps + 7) / 8), 256, 0, s>>>(p);
+  const int64_t all = static_cast<int64_t>(p.q_rows) * p.H;
+  packed_delta_kernel<<<static_cast<unsigned>((all + 63) / 64), 256, 0, s>>>(p);
   return check_launch();
 }
 

@@ -727,32 +727,41 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Merge the parts of the unit that begins in CTA blockIdx.x and ends in a later one: with
 // base b = max b_c and w_c = 2^(b_c - b), o = sum w_c o_c / sum w_c l_c, in CTA order. A
-// warp takes a row, a lane 4 of its 128 columns.
+// warp takes a row, a lane 4 of its 128 columns; the lanes first fetch the parts' bases and
+// sums side by side (32 at a time).
 __global__ void __launch_bounds__(256) packed_merge_kernel(const __grid_constant__ FwdParams p) {
   const Cut cut = p.cuts[blockIdx.x];
   if (!cut.crosses) return;
   const int lane = threadIdx.x & 31, step = gridDim.y * 8;
-  const int c0 = blockIdx.x;
+  const int c0 = blockIdx.x, parts = cut.last_cta - c0 + 1;
   for (int m = blockIdx.y * 8 + (threadIdx.x >> 5); m < cut.rows * p.pack; m += step) {
     const int query = m / p.pack, head = cut.group * p.pack + m - query * p.pack;
     const int t = query >= p.per_tile ? 1 : 0;
     const int in_slot = t * kPkTile + m - t * p.per_tile * p.pack;
-    auto slot_of = [&](int c) { return static_cast<int64_t>(c == c0 ? cut.first_slot : 2 * c) * p.slot_rows + in_slot; };
-    float base = -INFINITY;
-    for (int c = c0; c <= cut.last_cta; ++c) {
-      const float2 ml = p.part_ml[slot_of(c)];
-      if (ml.y != 0.f) base = fmaxf(base, ml.x);
-    }
-    float l = 0.f;
+    auto slot_of = [&](int i) { return static_cast<int64_t>(i == 0 ? cut.first_slot : 2 * (c0 + i)) * p.slot_rows + in_slot; };
+    float base = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0; c <= cut.last_cta; ++c) {
-      const int64_t slot = slot_of(c);
-      const float2 ml = p.part_ml[slot];
-      if (ml.y == 0.f) continue;
-      const float w = exp2f(ml.x - base);
-      const float4 v = reinterpret_cast<const float4*>(p.part_o + slot * kPkD)[lane];
-      l = fmaf(w, ml.y, l);
-      o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (i0 + lane < parts) ml = p.part_ml[slot_of(i0 + lane)];
+      if (ml.y == 0.f) ml.x = -INFINITY;  // a part that saw nothing
+      float top = ml.x;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      top = fmaxf(top, base);
+      const float back = base == -INFINITY ? 0.f : exp2f(base - top), w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
+      base = top;
+      l *= back;
+      o.x *= back, o.y *= back, o.z *= back, o.w *= back;
+      const int n = min(32, parts - i0);
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i), li = __shfl_sync(0xffffffffu, ml.y, i);
+        if (li == 0.f) continue;  // its output was not written
+        const float4 v = reinterpret_cast<const float4*>(p.part_o + slot_of(i0 + i) * kPkD)[lane];
+        l = fmaf(wi, li, l);
+        o.x = fmaf(wi, v.x, o.x), o.y = fmaf(wi, v.y, o.y), o.z = fmaf(wi, v.z, o.z), o.w = fmaf(wi, v.w, o.w);
+      }
     }
     const float inv = l == 0.f ? 0.f : 1.0f / l;
     const int64_t row = static_cast<int64_t>(cut.row0) + query;
@@ -779,24 +788,24 @@ SplitLayout split_layout(const PackedAttn& a) {
 
 }  // namespace
 
-int packed_heads_per_tile(int H, int Hk) {
+int packed_heads_per_tile(int H, int Hk, int rows) {
   const int group = H / Hk;
-  for (int n = group < kPkTile ? group : kPkTile; n > 1; --n)
+  for (int n = group < rows ? group : rows; n > 1; --n)
     if (group % n == 0) return n;
   return 1;
 }
 
-bool make_packed_q_map(CUtensorMap* map, const void* ptr, int64_t stride, int rows, int H, int pack) {
-  const uint64_t dims[3] = {kPkD, static_cast<uint64_t>(H), static_cast<uint64_t>(rows)};
+bool make_packed_q_map(CUtensorMap* map, const void* ptr, int64_t stride, int n_rows, int H, int pack, int tile_rows) {
+  const uint64_t dims[3] = {kPkD, static_cast<uint64_t>(H), static_cast<uint64_t>(n_rows)};
   const uint64_t strides[2] = {kPkD * 2, static_cast<uint64_t>(stride) * 2};
-  const uint32_t box[3] = {64, static_cast<uint32_t>(pack), static_cast<uint32_t>(kPkTile / pack)};
+  const uint32_t box[3] = {64, static_cast<uint32_t>(pack), static_cast<uint32_t>(tile_rows / pack)};
   return make_tmap_bf16(map, ptr, 3, dims, strides, box);
 }
 
-bool make_packed_kv_map(CUtensorMap* map, const void* ptr, int64_t stride, int rows, int Hk) {
-  const uint64_t dims[2] = {static_cast<uint64_t>(Hk) * kPkD, static_cast<uint64_t>(rows)};
+bool make_packed_kv_map(CUtensorMap* map, const void* ptr, int64_t stride, int n_rows, int Hk, int tile_rows) {
+  const uint64_t dims[2] = {static_cast<uint64_t>(Hk) * kPkD, static_cast<uint64_t>(n_rows)};
   const uint64_t strides[1] = {static_cast<uint64_t>(stride) * 2};
-  const uint32_t box[2] = {64, kPkTile};
+  const uint32_t box[2] = {64, static_cast<uint32_t>(tile_rows)};
   return make_tmap_bf16(map, ptr, 2, dims, strides, box);
 }
 
@@ -841,7 +850,7 @@ int launch_attn_packed_tc(const PackedAttn& a, void* ws, size_t ws_bytes, cudaSt
   (a.cap > 0.f || p.prescale ? packed_fwd_tc_kernel<false> : packed_fwd_tc_kernel<true>)<<<p.ctas, kThreads, kSmem, s>>>(mq, mk, mv, p);
   int st = check_launch();
   if (st == WAN_OK && p.may_split) {
-    packed_merge_kernel<<<dim3(p.ctas, 4), 256, 0, s>>>(p);
+    packed_merge_kernel<<<dim3(p.ctas, 16), 256, 0, s>>>(p);
     count_launches(1);
     st = check_launch();
   }

@@ -201,9 +201,9 @@ int launch_attn_packed_tc(const PackedAttn& p, void* ws, size_t ws_bytes, cudaSt
 size_t attn_packed_tc_workspace(const PackedAttn& p);
 // Heads of one key head that share a tile of packed query rows, and tensor maps of such
 // tiles ([128 rows / pack queries][pack heads][64 dims]) and of key tiles.
-int packed_heads_per_tile(int H, int Hk);
-bool make_packed_q_map(CUtensorMap* map, const void* ptr, int64_t stride, int rows, int H, int pack);
-bool make_packed_kv_map(CUtensorMap* map, const void* ptr, int64_t stride, int rows, int Hk);
+int packed_heads_per_tile(int H, int Hk, int rows = 128);
+bool make_packed_q_map(CUtensorMap* map, const void* ptr, int64_t stride, int n_rows, int H, int pack, int tile_rows = 128);
+bool make_packed_kv_map(CUtensorMap* map, const void* ptr, int64_t stride, int n_rows, int Hk, int tile_rows = 128);
 // The gradient's tensor-core kernels (delta already formed).
 int launch_attn_packed_tc_bwd(const PackedAttn& p, cudaStream_t s);
 // fp32 on the CUDA cores, head_dim <= 128; and the whole gradient of either type.

@@ -43,15 +43,16 @@ __device__ __forceinline__ T uniform(T v) {
 
 __device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
 
-// Zero rows [row0, 128) of a bf16 tile in shared memory, by one warp: rows behind a
-// document's end may hold anything (NaN too), and 0 * NaN would reach the sums. Whole rows
-// are cleared, so the swizzle inside a row does not matter. Ordered before tensor-core reads
-// of the tile that follow an arrival of this warp (after the call).
+// Zero rows [row0, kRows) of a bf16 tile (two spans of kRows swizzled rows) in shared memory, by
+// one warp: rows behind a document's end may hold anything (NaN too), and 0 * NaN would reach
+// the sums. Whole rows are cleared, so the swizzle inside a row does not matter. Ordered
+// before tensor-core reads of the tile that follow an arrival of this warp (after the call).
+template <int kRows = kPkTile>
 __device__ __forceinline__ void zero_tile_rows(uint8_t* tile, int row0) {
   const int lane = threadIdx.x & 31;
-  for (int i = row0 * 8 + lane; i < kPkTile * 8; i += 32) {
+  for (int i = row0 * 8 + lane; i < kRows * 8; i += 32) {
     *reinterpret_cast<uint4*>(tile + i * 16) = make_uint4(0, 0, 0, 0);
-    *reinterpret_cast<uint4*>(tile + kPkSpan + i * 16) = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(tile + kRows * 128 + i * 16) = make_uint4(0, 0, 0, 0);
   }
   fence_proxy_async_smem();
   __syncwarp();
