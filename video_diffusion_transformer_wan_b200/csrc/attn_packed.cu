@@ -15,8 +15,8 @@ int check_docs(const wan_dit_config* cfg, const wan_documents* d, int q_rows, in
   WAN_REQUIRE(kv_heads >= 1 && cfg->heads % kv_heads == 0 && cfg->heads <= 65535, WAN_ERR_SHAPE);
   WAN_REQUIRE(d->causal_block >= 0, WAN_ERR_SHAPE);
   WAN_REQUIRE(isfinite(d->scale) && isfinite(d->cap) && d->cap >= 0.f, WAN_ERR_SHAPE);
-  WAN_TRY(check_ptr(d->cu_q));
-  WAN_TRY(check_ptr(d->cu_k));
+  WAN_TRY(check_ints(d->cu_q, d->n_docs + 1));
+  WAN_TRY(check_ints(d->cu_k, d->n_docs + 1));
   WAN_TRY(check_opt_ptr(d->prefix));
   WAN_TRY(check_opt_ptr(d->slopes));
   return WAN_OK;

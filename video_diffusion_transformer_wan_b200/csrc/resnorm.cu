@@ -634,7 +634,7 @@ int check_op(const wan_dit_config* cfg, const wan_residual_norm* op, const float
   WAN_TRY(check_opt_ptr(op->w_post));
   WAN_TRY(check_opt_ptr(mod_bias));
   if (op->gate >= 0 || op->chunk >= 0) WAN_TRY(check_array(e, n_docs));
-  WAN_TRY(check_ptr(cu));
+  WAN_TRY(check_ints(cu, n_docs + 1));
   return WAN_OK;
 }
 

@@ -745,7 +745,7 @@ int check_common(const wan_dit_config* cfg, const wan_rope* rope, const int32_t*
   WAN_REQUIRE(rows >= 0 && kv_heads >= 1, WAN_ERR_SHAPE);
   WAN_REQUIRE(norm >= WAN_QK_NORM_NONE && norm <= WAN_QK_NORM_WIDTH, WAN_ERR_SHAPE);
   WAN_TRY(check_rope(rope, cfg->head_dim));
-  WAN_TRY(check_array(positions, rows));
+  WAN_TRY(check_ints(positions, rows));
   const int64_t n = static_cast<int64_t>(cfg->heads) + (with_k ? kv_heads : 0);
   WAN_REQUIRE(n <= kMaxHeads, WAN_ERR_UNSUPPORTED);
   return WAN_OK;
