@@ -40,7 +40,7 @@ constexpr int kDqStages = 5;
 constexpr int kDkvStages = 4;                // query tiles of 64 rows on their way
 constexpr int kHalfSpan = 64 * 128;          // 64 rows of one 128-byte swizzled span
 constexpr int kHalfBytes = 2 * kHalfSpan;    // 64 rows of 128 dims
-constexpr size_t kDqSmem = 1024 + static_cast<size_t>(kPkTileBytes) * (2 + kDqStages) + 512;
+constexpr size_t kDqSmem = 1024 + static_cast<size_t>(kPkTileBytes) * (2 + kDqStages) + 1280;
 // per staged query: float2 (log-sum, delta) or, with distances, float4; and a key count
 constexpr int kStatBytes = 64 * (16 + 4);
 constexpr int kStatBufs = 4;
@@ -101,8 +101,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* done = s_full + 3;
   uint64_t* ragged = s_full + 4;
   uint64_t* cleared = s_full + 5;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(s_full + 6);
-  int* found = reinterpret_cast<int*>(s_full + 7);
+  uint64_t* halves = s_full + 6;            // both halves' parts of delta are there
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(s_full + 7);
+  int* found = reinterpret_cast<int*>(s_full + 8);
+  float* part = reinterpret_cast<float*>(s_full + 10);  // [2][128]
 
   int di, tile;
   if (!cta_tile(p.a.cu_q, p.a.n_docs, p.a.q_rows, p.per_tile, found, di, tile)) return;
@@ -120,6 +122,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(done, 1);
     mbar_init(ragged, 1);
     mbar_init(cleared, 1);
+    mbar_init(halves, kScoreThreads);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -212,7 +215,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool live = query < rows;
     const int seen = live ? seen_keys(i, doc.off, doc.Lk, doc.prefix, p.a.causal_block) : 0x7fffffff;
     const int64_t stat = static_cast<int64_t>(head) * p.a.q_rows + doc.q0 + i;
-    const float nl = live ? -p.a.lse[stat] * kLog2e : 0.f, nd = live ? -p.a.delta[stat] : 0.f;
+    const float nl = live ? -p.a.lse[stat] * kLog2e : 0.f;
+    float nd = live ? -p.a.delta[stat] : 0.f;
     const float slope2 = !kPlain && p.a.slopes && live ? __ldg(p.a.slopes + head) * kLog2e : 0.f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
@@ -231,9 +235,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       mbar_arrive(y_free);
       const int key0 = j * kPkTile + 64 * half;
-      const unsigned long long nl2 = f2_splat(nl), nd2 = f2_splat(nd), mult2 = f2_splat(p.mult);
+      const unsigned long long nl2 = f2_splat(nl), mult2 = f2_splat(p.mult);
+      const float from = static_cast<float>(i + doc.off - key0);
+      const int valid = seen - key0;
+      auto log2_p = [&](int c) {
+        const unsigned long long y = f2_fma(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), mult2, nl2);
+        if (kPlain || !p.a.slopes) return f2_unpack(y);
+        return f2_unpack(f2_add(y, f2_pack(-slope2 * fabsf(from - static_cast<float>(c)), -slope2 * fabsf(from - static_cast<float>(c + 1)))));
+      };
+      if (!kPlain && p.a.cap > 0.f) cap_scores(s, p.cap_in, live);
+      if (n == 1) {
+        // All keys of the row are at hand: delta = sum(p dp) itself, since with few keys the
+        // rounding of o to bf16 weighs in do * o (dq and dk of documents of 2 keys were 2.3
+        // times as far off as the plain form's). The keys' kernel takes it from here too.
+        float sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          const float2 e = log2_p(c);
+          if (c < valid) sum = fmaf(ex2_approx(e.x), __uint_as_float(g[c]), sum);
+          if (c + 1 < valid) sum = fmaf(ex2_approx(e.y), __uint_as_float(g[c + 1]), sum);
+        }
+        part[half * kPkTile + row] = sum;
+        mbar_arrive(halves);
+        if (!mbar_wait_warp(halves, 0, p.err)) {
+          ok = false;
+          break;
+        }
+        nd = -(part[row] + part[kPkTile + row]);
+        if (live && half == 0) p.a.delta[stat] = -nd;
+      }
+      const unsigned long long nd2 = f2_splat(nd);
       if (!kPlain && p.a.cap > 0.f) {
-        cap_scores(s, p.cap_in, live);
 #pragma unroll
         for (int c = 0; c < 64; c += 2) {  // g = (dp - delta)(1 - t^2)
           const unsigned long long t = f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
@@ -248,18 +280,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           g[c] = __float_as_uint(v.x), g[c + 1] = __float_as_uint(v.y);
         }
       }
-      const float from = static_cast<float>(i + doc.off - key0);
 #pragma unroll
       for (int c = 0; c < 64; c += 2) {
-        unsigned long long y = f2_fma(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), mult2, nl2);
-        if (!kPlain && p.a.slopes)
-          y = f2_add(y, f2_pack(-slope2 * fabsf(from - static_cast<float>(c)), -slope2 * fabsf(from - static_cast<float>(c + 1))));
-        const float2 e = f2_unpack(y);
+        const float2 e = log2_p(c);
         const float2 d = f2_unpack(f2_mul(f2_pack(ex2_approx(e.x), ex2_approx(e.y)),
                                           f2_pack(__uint_as_float(g[c]), __uint_as_float(g[c + 1]))));
         s[c] = __float_as_uint(d.x), s[c + 1] = __float_as_uint(d.y);
       }
-      const int valid = seen - key0;
       if (__any_sync(0xffffffffu, valid < 64)) {
 #pragma unroll
         for (int c = 0; c < 64; ++c)
