@@ -850,7 +850,7 @@ int launch_attn_packed_tc(const PackedAttn& a, void* ws, size_t ws_bytes, cudaSt
   (a.cap > 0.f || p.prescale ? packed_fwd_tc_kernel<false> : packed_fwd_tc_kernel<true>)<<<p.ctas, kThreads, kSmem, s>>>(mq, mk, mv, p);
   int st = check_launch();
   if (st == WAN_OK && p.may_split) {
-    packed_merge_kernel<<<dim3(p.ctas, 16), 256, 0, s>>>(p);
+    packed_merge_kernel<<<dim3(p.ctas, l.slot_rows < 128 ? (l.slot_rows + 7) / 8 : 16), 256, 0, s>>>(p);
     count_launches(1);
     st = check_launch();
   }
