@@ -19,7 +19,7 @@
 // collide), and are added in order by a second kernel: no atomics. Statistics are fp32, squares
 // about a mean (the row's, or, in the gradient, the warp's and then moved). What bounds them
 // now are the barriers and the latencies between them: forward 130 us for 604 MB (4.6 TB/s,
-// 32,760 rows of 1536), gradient 565 us for 2.07 GB (3.7 TB/s, 22,501 rows of 5120; 1263 us
+// 32,760 rows of 1536), gradient 545 us for 2.07 GB (3.8 TB/s, 22,501 rows of 5120; 1263 us
 // with five barriers a row and the sums in registers).
 #include <cuda_bf16.h>
 
