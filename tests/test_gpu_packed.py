@@ -46,6 +46,8 @@ ROPE = [
     (19, 4, 2, 32, [6, 10], {}, "half", "head"),       # quads do not divide the halves
     (40, 64, 32, 2, [2], {}, "interleaved", "width"),  # one pair a head
     (13, 7, 7, 64, [10], {}, "half", "width"),
+    (50, 20, 20, 128, [128], {}, "half", "width"),     # 2560 columns a side
+    (21, 48, 48, 128, [64, 64], {}, "interleaved", "width"),
 ]
 
 

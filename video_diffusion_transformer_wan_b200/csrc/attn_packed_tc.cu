@@ -49,8 +49,10 @@ static_assert(128 * kRegsLow + 256 * kRegsHigh <= 384 * 168, "register split abo
 constexpr int kThreads = 384;
 constexpr int kStages = 5;
 constexpr int kMaxCtas = 148;
-constexpr int kMinSplit = 8;         // a unit of more key tiles may be cut
-constexpr int kMinShare = 4;         // key tiles a CTA takes at least
+// A unit of more key tiles may be cut: a cut costs its parts' way through memory (ragged texts
+// 86 us with 2 against 73; single tokens over long keys 69 with 2, 71 with 8, 82 with 16).
+constexpr int kMinSplit = 8;
+constexpr int kMinShare = 4;         // key tiles a CTA takes at least (12: ragged texts 82 us)
 constexpr int kUnitCost = 2;         // see unit_weight
 constexpr float kRescaleLog2 = 8.0f;
 constexpr int kPolyEvery = 8;        // one pair of exponentials in this many runs on the FMA pipes

@@ -14,10 +14,11 @@
 // exchanges and waited at barriers: 108 us against 75 us forward, 179 against 154 us gradient, on
 // 32,760 and 27,569 rows of 12 + 12 heads.) The cosines of a row are made once per pair, the
 // turns reduced in fp64 (positions may be far) and the sine taken in fp32. Up to 6 x 256 columns
-// of a side stay in registers between the norm's sums and their use; wider rows are read
-// twice, the second time from the caches.
+// of a side (forward: 20 x 256) stay in registers between the norm's sums and their use; wider
+// rows are read twice, the second time from the caches.
 // qk_norm_rope_any_kernel serves what this layout does not divide: rows that are not 16-byte
-// aligned, heads that do not divide 256 dims or are below 8, halves of odd quads.
+// aligned, heads that do not divide 256 dims or are below 8, halves of odd quads (on the rows
+// above it takes 332 us forward and 1553 us for the gradient).
 #include <cuda_bf16.h>
 
 #include <math.h>
@@ -262,6 +263,9 @@ using F2 = unsigned long long;  // two fp32
 constexpr int kMaxHeads = 96;  // q and k heads of one row together
 constexpr int kWarps = 8;      // per block
 constexpr int kHeld = 6;       // groups of 256 columns that stay in registers
+// More of them in the forward (read twice: 143, 161 and 268 us for 20, 24 and 40 heads of q and
+// of k on 20,000 rows; held: 98, 106 and 153), the last only of two bytes each.
+constexpr int kHeldMore = 12, kHeldMost = 20;
 
 // A thread's 8 columns of a head: two quads at da and db; pairs (da + 2k, da + 2k + 1), or,
 // split, (da + k, db + k).
@@ -693,7 +697,12 @@ int launch_vec(const RopeParams& p, RopePlan& pl, bool dw, cudaStream_t s) {
 template <typename T, bool kHalf, bool kBwd>
 int run_vec(const RopeParams& p, RopePlan& pl, bool dw, cudaStream_t s) {
   const int widest = (p.H > p.n - p.H ? p.H : p.n - p.H) * p.d;
-  return widest <= kHeld * 256 ? launch_vec<T, kHeld, kHalf, kBwd>(p, pl, dw, s) : launch_vec<T, 0, kHalf, kBwd>(p, pl, dw, s);
+  if (widest <= kHeld * 256) return launch_vec<T, kHeld, kHalf, kBwd>(p, pl, dw, s);
+  if constexpr (!kBwd) {
+    if (widest <= kHeldMore * 256) return launch_vec<T, kHeldMore, kHalf, kBwd>(p, pl, dw, s);
+    if (sizeof(T) == 2 && widest <= kHeldMost * 256) return launch_vec<T, sizeof(T) == 2 ? kHeldMost : 0, kHalf, kBwd>(p, pl, dw, s);
+  }
+  return launch_vec<T, 0, kHalf, kBwd>(p, pl, dw, s);
 }
 
 int check_rope(const wan_rope* r, int head_dim) {

@@ -86,12 +86,11 @@ def _torch():
     return _TORCH
 
 
-def _stream(stream):
-    """The stream given, or the current one of the current device."""
+def _stream(stream, device):
+    """The stream given, or the device's current one."""
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    torch = _torch()
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return _torch()._C._cuda_getCurrentRawStream(device)
 
 
 def _act(cfg):
@@ -136,10 +135,10 @@ class _Args:
                 self.fail(f"{name} is required")
             return None
         self._seen(t, name)
-        if t.dtype != dtype or t.shape != (n, width) or (width > 1 and t.stride(1) != 1):
-            self.fail(f"{name} must be {dtype} [{n}, {width}] with dense rows, got {t.dtype} {tuple(t.shape)} strides "
-                      f"{t.stride()}")
-        stride = t.stride(0) if n > 1 else width  # the stride of a single row says nothing
+        st = t.stride()
+        if t.dtype != dtype or t.shape != (n, width) or (st[1] != 1 and width > 1):
+            self.fail(f"{name} must be {dtype} [{n}, {width}] with dense rows, got {t.dtype} {tuple(t.shape)} strides {st}")
+        stride = st[0] if n > 1 else width  # the stride of a single row says nothing
         return ctypes.byref(Rows(t.data_ptr(), stride))
 
     def workspace(self, ws):
@@ -151,12 +150,16 @@ class _Args:
         return ws.data_ptr(), ws.numel() * ws.element_size()
 
     def call(self, fn, stream, *args):
-        cuda, f = _torch().cuda, getattr(_lib(), fn)
-        if self.device == cuda.current_device():
-            _check(f(*args, _stream(stream)), fn)
-            return
-        with cuda.device(self.device):
-            _check(f(*args, _stream(stream)), fn)
+        f, torch, dev = getattr(_lib(), fn), _torch(), self.device
+        if dev < 0:  # a call without tensors
+            dev = torch.cuda.current_device()
+        if dev == torch._C._cuda_getDevice():
+            status = f(*args, _stream(stream, dev))
+        else:
+            with torch.cuda.device(dev):
+                status = f(*args, _stream(stream, dev))
+        if status != 0:
+            _check(status, fn)
 
 
 def _choice(table, value, name):
