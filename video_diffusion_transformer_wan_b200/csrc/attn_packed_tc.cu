@@ -586,9 +586,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait();
         if (!kPlain && p.a.cap > 0.f) cap_scores(r, p.cap_in, live);
         if (!kPlain && p.prescale) {
+          const unsigned long long m2 = f2_splat(p.mult);
+          if (__all_sync(0xffffffffu, !live || from >= kPkTile - 1 || from <= 0.f)) {
+            // every key lies on one side of the row's own place: the distance is linear
+            const float w = from > 0.f ? slope2 : -slope2, b = -w * from;
 #pragma unroll
-          for (int c = 0; c < kPkTile; ++c)
-            r[c] = __float_as_uint(fmaf(__uint_as_float(r[c]), p.mult, -slope2 * fabsf(from - static_cast<float>(c))));
+            for (int c = 0; c < kPkTile; c += 2) {
+              const float2 v = f2_unpack(f2_fma(f2_pack(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), m2,
+                                                f2_pack(fmaf(w, static_cast<float>(c), b), fmaf(w, static_cast<float>(c + 1), b))));
+              r[c] = __float_as_uint(v.x), r[c + 1] = __float_as_uint(v.y);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < kPkTile; ++c)
+              r[c] = __float_as_uint(fmaf(__uint_as_float(r[c]), p.mult, -slope2 * fabsf(from - static_cast<float>(c))));
+          }
         }
         const bool cut = __any_sync(0xffffffffu, valid < kPkTile);
         if (cut) {
