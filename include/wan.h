@@ -505,7 +505,8 @@ size_t wan_attention_fp8_workspace_bytes(const wan_dit_config* cfg, int B, int L
  * batch of clips of mixed sizes, needs beside wan_adaln_modulate, wan_linear_fwd and
  * wan_attention_fwd, with their gradients. Tensors of one call must not overlap unless a
  * call says so. Offsets are 64-bit: a tensor may exceed 2^31 elements; row counts are int.
- * Arrays of offsets and positions need 4-byte alignment only (a slice of one will do).
+ * Arrays of offsets and positions need 4-byte alignment only (a slice of one will do). A
+ * workspace serves one call at a time: calls that may overlap (two streams) need one each.
  * All results are the same from run to run (no atomics on floating-point values). */
 
 /* Rows of a tensor: row r starts at ptr + r * row_stride elements. ptr is 16-byte

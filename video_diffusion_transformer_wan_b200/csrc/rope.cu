@@ -40,7 +40,7 @@ struct RopeParams {
   void *q_out, *k_out;
   const void *gq, *gk;  // gradient: dq_out, dk_out
   int64_t q_stride, k_stride, qo_stride, ko_stride, gq_stride, gk_stride;
-  float* part;          // gradient: [block][tb * n][head_dim] partial weight gradients
+  float* part;          // gradient: the blocks' partial rows of the weights' gradients
   const int32_t* pos;
   int rows, H, n, d, tb, norm, layout, pairs, n_axes;  // n = heads of q and k together
   float eps, amplitude;
