@@ -194,6 +194,31 @@ def test_more_query_heads_than_a_tile_has_rows(wan, H, Hk):
         R.assert_close(t, *want[name], name)
 
 
+@pytest.mark.parametrize("lens,H,Hk,causal", [([520] * 40 + [3, 0, 700], 64, 64, 0),   # more long documents than are walked in waves
+                                              ([1, 3, 0, 2] * 175, 2, 1, 1)])         # hundreds of short ones
+def test_many_documents(wan, lens, H, Hk, causal):
+    d, n = 128, sum(lens)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    q, k, v, do = (torch.randn(n, h * d, generator=g, device="cuda").bfloat16() for h in (H, Hk, Hk, H))
+    cfg, docs, cu = wan.make_config(H * d, H, 64), wan.documents(_i32(R.cu_of(lens)), causal_block=causal), R.cu_of(lens)
+    ws = torch.empty(wan.attention_packed_workspace_bytes(cfg, n, n, len(lens), Hk, True), dtype=torch.uint8, device="cuda")
+    o, lse = torch.empty_like(q), torch.empty(H, n, device="cuda")
+    want = R.attention(q.double(), k.double(), v.double(), H, Hk, cu, cu, torch.bfloat16,
+                       do=do.double() if causal else None, block=causal)
+    for w in (ws, None):
+        o.fill_(7.0)
+        wan.attention_packed_fwd(cfg, docs, q, k, v, o, lse, kv_heads=Hk, ws=w)
+        assert wan.device_status() == 0
+        R.assert_close(o, *want["o"], "o")
+        R.assert_close(lse, *want["lse"], "lse")
+    if causal:
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        wan.attention_packed_bwd(cfg, docs, q, k, v, o, lse, do, dq, dk, dv, kv_heads=Hk, ws=ws)
+        assert wan.device_status() == 0
+        for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
+            R.assert_close(t, *want[name], name)
+
+
 def test_offsets_past_32_bits(wan):
     """A qkv tensor of more than 2^31 elements whose documents lie at its end."""
     H, d, n = 12, 128, 480000
