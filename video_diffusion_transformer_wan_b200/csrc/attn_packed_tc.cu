@@ -311,12 +311,14 @@ __device__ __forceinline__ bool walk_step(Walk& w, const FwdParams& p, const Sha
   w.at = at, w.weight = weight;
   return false;
 }
-// The same for a whole warp.
+// The same for a whole warp. The barriers order the other lanes' reads of the piece before with
+// lane 0's writes, and those with the reads that follow: a shuffle alone orders no memory.
 __device__ __forceinline__ bool walk_next(Walk& w, const FwdParams& p, const Share& s) {
   __syncwarp();
   bool more = false;
   if ((threadIdx.x & 31) == 0) more = walk_step(w, p, s);
-  return __shfl_sync(0xffffffffu, more, 0);  // orders the step before the other lanes' reads too
+  __syncwarp();
+  return __shfl_sync(0xffffffffu, more, 0);
 }
 
 // Ring position of K_j / V_j in the load order K_0, K_1, V_0, K_2, V_1, ..., V_{n-1}.
