@@ -1,0 +1,64 @@
+"""Packed-document operators at their edges: what neighbours and unused rows hold, empty
+documents and batches, head dims and scales other than the usual ones, cut units of every kind."""
+import math
+
+import pytest
+
+import packed_ref as R
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+ACT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def wan():
+    import video_diffusion_transformer_wan_b200 as w
+    return w
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def _attention(wan, cfg, docs, q, k, v, Hk, do=None, split=True):
+    """o, lse (and dq, dk, dv) of one call; rows that are not written hold 7."""
+    H, n = cfg.heads, docs.n_docs
+    size = wan.attention_packed_workspace_bytes(cfg, q.shape[0], k.shape[0], n, Hk, do is not None)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda") if size else None
+    full = lambda t: torch.full(t.shape, 7.0, dtype=t.dtype, device="cuda")  # noqa: E731
+    out = dict(o=full(q), lse=torch.full((H, q.shape[0]), 7.0, device="cuda"))
+    wan.attention_packed_fwd(cfg, docs, q, k, v, out["o"], out["lse"], kv_heads=Hk, ws=ws if split else None)
+    if do is not None:
+        out.update(dq=full(q), dk=full(k), dv=full(v))
+        wan.attention_packed_bwd(cfg, docs, q, k, v, out["o"], out["lse"], do, out["dq"], out["dk"], out["dv"],
+                                 kv_heads=Hk, ws=ws)
+    assert wan.device_status() == 0
+    return out
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("block,slopes", [(0, False), (1, True)])
+def test_neighbours_do_not_reach_a_document(wan, dtype, block, slopes):
+    """The same document in front of neighbours of size 1 and of size 1e4 (and rows of no document
+    alike): every bit of its results is the same, with capped scores too."""
+    H, Hk, d, act, lens = 4, 2, 128 if dtype == "bf16" else 64, ACT[dtype], [70, 90]
+    n = sum(lens) + 20
+    cfg = wan.make_config(H * d, H, 64, dtype=dtype)
+    docs = wan.documents(_i32(R.cu_of(lens)), causal_block=block, cap=15.0,
+                         slopes=torch.tensor([0.5, 0.25, 0.125, 0.0625], device="cuda") if slopes else None)
+    got = []
+    for big in (1.0, 1e4):
+        g = _gen(7)
+        q, k, v, do = (torch.randn(n, h * d, generator=g, device="cuda") for h in (H, Hk, Hk, H))
+        for t in (q, k, v, do):
+            t[lens[0]:] *= big
+        got.append(_attention(wan, cfg, docs, *(t.to(act) for t in (q, k, v)), Hk, do=do.to(act)))
+    for name in got[0]:
+        a, b = (t[name][:, :lens[0]] if name == "lse" else t[name][:lens[0]] for t in got)
+        assert torch.equal(a, b), name

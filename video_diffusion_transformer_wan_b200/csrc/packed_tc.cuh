@@ -98,16 +98,20 @@ __device__ __forceinline__ float tanh_exp(float y) {
   const float e = ex2_approx(2.0f * kLog2e * fabsf(y));
   return copysignf(1.0f - __fdividef(2.0f, e + 1.0f), y);
 }
-// In place over N scores s: tanh(s * c). The polynomial serves a warp whose scores all stay
-// under half the cap (ordinary ones do); one exponential and one reciprocal each otherwise.
-// Rows that are not `live` hold anything and do not decide.
+// In place over N scores s: tanh(s * c), by the polynomial where |s c| <= 1/2 and by the
+// exponential elsewhere: a score's bits depend on it alone, whatever stands beside it (columns
+// that the row does not see may hold anything), and the gradient forms the forward's. A warp whose
+// scores all stay under half the cap (ordinary ones do) leaves the exponentials out; with them 9,360
+// frame-causal rows of 12 heads take 512 us against 302. (Columns not seen kept out of the vote too:
+// 322 us, 4 to 5 % of every call, for the time of those beside large neighbours.) Rows that are not
+// `live` do not decide.
 template <int N>
 __device__ __forceinline__ void cap_scores(uint32_t (&r)[N], float c, bool live) {
   float big = 0.f;
 #pragma unroll
   for (int i = 0; i < N; i += 2) big = fmax3(big, fabsf(__uint_as_float(r[i])), fabsf(__uint_as_float(r[i + 1])));
+  const unsigned long long c2 = f2_splat(c);
   if (__all_sync(0xffffffffu, !live || big * fabsf(c) <= kTanhPolyLimit)) {
-    const unsigned long long c2 = f2_splat(c);
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
       const float2 t = f2_unpack(tanh_poly2(f2_mul(f2_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), c2)));
@@ -115,7 +119,12 @@ __device__ __forceinline__ void cap_scores(uint32_t (&r)[N], float c, bool live)
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = __float_as_uint(tanh_exp(__uint_as_float(r[i]) * c));
+    for (int i = 0; i < N; i += 2) {
+      const unsigned long long y2 = f2_mul(f2_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), c2);
+      const float2 y = f2_unpack(y2), t = f2_unpack(tanh_poly2(y2));
+      r[i] = __float_as_uint(fabsf(y.x) <= kTanhPolyLimit ? t.x : tanh_exp(y.x));
+      r[i + 1] = __float_as_uint(fabsf(y.y) <= kTanhPolyLimit ? t.y : tanh_exp(y.y));
+    }
   }
 }
 
