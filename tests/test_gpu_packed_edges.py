@@ -62,3 +62,28 @@ def test_neighbours_do_not_reach_a_document(wan, dtype, block, slopes):
     for name in got[0]:
         a, b = (t[name][:, :lens[0]] if name == "lse" else t[name][:lens[0]] for t in got)
         assert torch.equal(a, b), name
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_modulation_of_an_empty_document_is_not_used(wan, dtype, bad):
+    """Unused slots of a batch of fixed size: whatever their modulation holds, no sum sees it."""
+    lens, D, act = [3, 0, 5, 0], 128, ACT[dtype]
+    n, g = sum(lens), _gen(2)
+    rnd = lambda *s, t=torch.float32: torch.randn(*s, generator=g, device="cuda").to(t)  # noqa: E731
+    cfg = wan.make_config(D, 2, 64, dtype=dtype)
+    w = [rnd(D, t=act) for _ in range(3)]
+    spec = wan.residual_norm(pre="layer", post="rms", gate=2, chunk=1, w_pre=w[0], b_pre=w[1], w_post=w[2])
+    x, y, e, mb, dh, up = rnd(n, D), rnd(n, D, t=act), rnd(4, 6, D), rnd(6, D), rnd(n, D, t=act), rnd(n, D)
+    ws = torch.empty(wan.gated_residual_norm_workspace_bytes(cfg, n, 4), dtype=torch.uint8, device="cuda")
+    got = []
+    for fill in (0.0, bad):
+        e[1], e[3] = fill, fill
+        sums = dict(de=torch.zeros(4, 6, D, device="cuda"), dmod_bias=torch.zeros(6, D, device="cuda"),
+                    **{k: torch.empty(D, device="cuda") for k in ("dw_pre", "db_pre", "dw_post")})
+        dx, dy = torch.empty(n, D, device="cuda"), torch.empty(n, D, dtype=act, device="cuda")
+        wan.gated_residual_norm_bwd(cfg, spec, x, y, e, mb, _i32(R.cu_of(lens)), dh, up, dx, dy, ws, **sums)
+        got.append(dict(dx=dx, dy=dy, **sums))
+    for name in got[0]:
+        assert torch.isfinite(got[1][name]).all() and torch.equal(got[0][name], got[1][name]), name
+    assert not got[1]["de"][1].any() and not got[1]["de"][3].any()

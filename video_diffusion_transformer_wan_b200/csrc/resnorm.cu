@@ -547,6 +547,7 @@ __global__ void __launch_bounds__(128) resnorm_weight_sums_kernel(const ResNormP
   float dw = 0.f, db = 0.f, dwp = 0.f, m0 = 0.f, m1 = 0.f, m2 = 0.f;
   const float w = at<T>(p.w_pre, c, 1.f), b = at<T>(p.b_pre, c, 0.f), wp = at<T>(p.w_post, c, 1.f);
   for (int doc = 0; doc < p.n_docs; ++doc) {
+    if (doc_range(p.cu, doc, p.rows).count == 0) continue;  // its modulation may hold anything: 0 * NaN
     const float* t = total + static_cast<int64_t>(doc) * 3 * p.D + c;
     const float S0 = t[0], S1 = t[p.D], S2 = t[2 * static_cast<int64_t>(p.D)];
     const float s1 = p.chunk >= 0 ? 1.f + mod_at(p, doc, 3 * p.chunk + 1, c) : 1.f;
