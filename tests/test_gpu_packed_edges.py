@@ -87,3 +87,19 @@ def test_modulation_of_an_empty_document_is_not_used(wan, dtype, bad):
     for name in got[0]:
         assert torch.isfinite(got[1][name]).all() and torch.equal(got[0][name], got[1][name]), name
     assert not got[1]["de"][1].any() and not got[1]["de"][3].any()
+
+
+def test_gradient_with_warps_of_uneven_pace(wan):
+    """One query (one warp of scores has work, the others none) over many key tiles, scores on both
+    sides of half the cap: the same bits from run to run, within the bounds."""
+    H, d, nk = 4, 128, 9000
+    g = _gen(3)
+    q, k, v, do = (torch.randn(n, H * d, generator=g, device="cuda").bfloat16() for n in (1, nk, nk, 1))
+    cfg, docs = wan.make_config(H * d, H, 64), wan.documents(_i32([0, 1]), _i32([0, nk]), cap=5.0)
+    want = R.attention(*(t.double() for t in (q, k, v)), H, H, [0, 1], [0, nk], torch.bfloat16, do=do.double(), cap=5.0)
+    first = _attention(wan, cfg, docs, q, k, v, H, do=do)
+    for name in first:
+        R.assert_close(first[name], *want[name], name)
+    for _ in range(200):
+        again = _attention(wan, cfg, docs, q, k, v, H, do=do)
+        assert all(torch.equal(again[name], first[name]) for name in first)

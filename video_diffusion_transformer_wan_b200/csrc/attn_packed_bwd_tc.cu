@@ -110,14 +110,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* kv_empty = kv_full + kDqStages;
   uint64_t* s_full = kv_empty + kDqStages;  // S(j) and dP(j) are there
   uint64_t* y_free = s_full + 1;            // dP(j) has been read
+  // [2] ds(j) is in place (j & 1): S(j+1) and dP(j+1) do not wait for ds(j), so a warp may be a tile
+  // ahead of another, and on one barrier its arrival would stand for the late one's.
   uint64_t* ds_full = s_full + 2;
-  uint64_t* done = s_full + 3;
-  uint64_t* ragged = s_full + 4;
-  uint64_t* cleared = s_full + 5;
-  uint64_t* halves = s_full + 6;            // both halves' parts of delta are there
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(s_full + 7);
-  int* found = reinterpret_cast<int*>(s_full + 8);
-  float* part = reinterpret_cast<float*>(s_full + 10);  // [2][128]
+  uint64_t* done = s_full + 4;
+  uint64_t* ragged = s_full + 5;
+  uint64_t* cleared = s_full + 6;
+  uint64_t* halves = s_full + 7;            // both halves' parts of delta are there
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(s_full + 8);
+  int* found = reinterpret_cast<int*>(s_full + 9);
+  float* part = reinterpret_cast<float*>(s_full + 11);  // [2][128]
+  static_assert(8 * (1 + 2 * kDqStages + 11) + 2 * kPkTile * 4 <= 1280, "barriers and parts");
 
   int di, tile;
   if (!cta_tile(p.a.cu_q, p.a.n_docs, p.a.q_rows, p.per_tile, found, di, tile)) return;
@@ -131,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kDqStages; ++s) mbar_init(&kv_full[s], 1), mbar_init(&kv_empty[s], 1);
     mbar_init(s_full, 1);
     mbar_init(y_free, kScoreThreads);
-    mbar_init(ds_full, kScoreThreads);
+    for (int b = 0; b < 2; ++b) mbar_init(&ds_full[b], kScoreThreads);
     mbar_init(done, 1);
     mbar_init(ragged, 1);
     mbar_init(cleared, 1);
@@ -207,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = mbar_wait_warp(q_full, 0, p.err) && scores(0);
       for (int j = 0; ok && j < nu; ++j) {
         if (j + 1 < nu && !scores(j + 1)) break;
-        if (!mbar_wait_warp(ds_full, static_cast<uint32_t>(j & 1), p.err)) break;
+        if (!mbar_wait_warp(&ds_full[j & 1], static_cast<uint32_t>((j >> 1) & 1), p.err)) break;
         tc_fence_after();
         const uint64_t kd = kt_desc + stage_off(2 * j);
         if (elect_lane()) {
@@ -312,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_st32(x, *reinterpret_cast<uint32_t(*)[32]>(s));
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(ds_full);
+      mbar_arrive(&ds_full[j & 1]);
     }
     if (ok && n > 0) ok = mbar_wait_warp(done, 0, p.err);
     if (ok) {
