@@ -103,3 +103,30 @@ def test_gradient_with_warps_of_uneven_pace(wan):
     for _ in range(200):
         again = _attention(wan, cfg, docs, q, k, v, H, do=do)
         assert all(torch.equal(again[name], first[name]) for name in first)
+
+
+@pytest.mark.parametrize("rows,n_docs", [(0, 0), (0, 2), (4, 0)])
+def test_residual_norm_gradient_of_nothing(wan, rows, n_docs):
+    """No rows, no documents, or neither, with the workspace that the sizing call asks for: the sums
+    are zeros, rows of no document stay as they were, and only what ran is counted."""
+    D = 128
+    cfg, spec = wan.make_config(D, 2, 64, dtype="f32"), wan.residual_norm(pre="layer", post="rms", gate=2, chunk=1)
+    full = lambda *s: torch.full(s, 7.0, device="cuda")  # noqa: E731
+    x, y, dx, dy = (full(rows, D) for _ in range(4))
+    e, mb, cu = full(n_docs, 6, D), full(6, D), _i32([0] * (n_docs + 1))
+    ws = torch.empty(wan.gated_residual_norm_workspace_bytes(cfg, rows, n_docs), dtype=torch.uint8, device="cuda")
+    assert (ws.numel() == 0) == (rows == 0 and n_docs == 0)
+    sums = dict(de=full(n_docs, 6, D), dmod_bias=full(6, D), dw_pre=full(D), db_pre=full(D), dw_post=full(D))
+    before = wan.launch_count()
+    wan.gated_residual_norm_bwd(cfg, spec, x, y, e, mb, cu, x, None, dx, dy, ws, **sums)
+    torch.cuda.synchronize()
+    assert wan.launch_count() - before == (3 if n_docs else 1)
+    assert (dx == 7).all() and (dy == 7).all()
+    for name in ("dw_pre", "db_pre", "dw_post"):
+        assert not sums[name].any(), name
+    for name in ("de", "dmod_bias"):
+        t = sums[name]
+        assert not t[..., 2:5, :].any() and (t[..., :2, :] == 7).all() and (t[..., 5, :] == 7).all(), name
+    before = wan.launch_count()
+    wan.gated_residual_norm_bwd(cfg, spec, x, y, e, mb, cu, x, None, dx, dy, ws)
+    assert wan.launch_count() == before

@@ -605,18 +605,21 @@ int launch_bwd(const ResNormParams& p, cudaStream_t s, int* blocks) {
 }
 template <typename T>
 int run_bwd(const ResNormParams& p, const wan_residual_norm_grads& g, float* total, cudaStream_t s) {
+  const bool weights = g.dmod_bias || g.dw_pre || g.db_pre || g.dw_post;
   int blocks = 0, st = WAN_OK;
   if (p.n_docs > 0)
     st = p.D <= 2048 ? launch_bwd<T, 1, 256, 3>(p, s, &blocks)
                      : p.D <= 5120 ? launch_bwd<T, 2, 320, 2>(p, s, &blocks) : launch_bwd<T, 2, 512, 1>(p, s, &blocks);
-  if (st != WAN_OK || !p.part) return st;
+  else
+    count_launches(-1);  // the call was counted as one
+  if (st != WAN_OK || !(weights || g.de)) return st;
   if (p.n_docs > 0) {
     const int docs_y = p.n_docs < 1024 ? p.n_docs : 1024;
     resnorm_doc_sums_kernel<T><<<dim3((p.D + 31) / 32, docs_y), dim3(32, 32), 0, s>>>(p, blocks, total, g.de);
     count_launches(1);
     st = check_launch();
   }
-  if (st != WAN_OK || !(g.dmod_bias || g.dw_pre || g.db_pre || g.dw_post)) return st;
+  if (st != WAN_OK || !weights) return st;
   resnorm_weight_sums_kernel<T><<<(p.D + 127) / 128, 128, 0, s>>>(p, total, g);
   count_launches(1);
   return check_launch();
@@ -709,8 +712,9 @@ int wan_gated_residual_norm_bwd(const wan_dit_config* cfg, const wan_residual_no
   p.dh = dh, p.dx_out = dx_out, p.dx = dx, p.dy = dy;
   float* total = nullptr;
   if (sums) {
-    WAN_TRY(check_ptr(workspace));
-    WAN_REQUIRE(ws_bytes >= wan_gated_residual_norm_workspace_bytes(cfg, rows, n_docs), WAN_ERR_WORKSPACE);
+    const size_t need = wan_gated_residual_norm_workspace_bytes(cfg, rows, n_docs);
+    if (need > 0) WAN_TRY(check_ptr(workspace));  // no rows and no documents: none
+    WAN_REQUIRE(ws_bytes >= need, WAN_ERR_WORKSPACE);
     p.part = static_cast<float*>(workspace);
     const int64_t blocks = rows < kMaxBlocks ? rows : kMaxBlocks;
     total = p.part + (blocks + n_docs) * 3 * static_cast<int64_t>(cfg->dim);
