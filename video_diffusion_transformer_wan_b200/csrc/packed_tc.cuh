@@ -61,7 +61,8 @@ __device__ __forceinline__ void zero_tile_rows(uint8_t* tile, int row0) {
 // A pair of 2^x on the FMA pipes, x from -125 up (below: 2^-125; NaN stays NaN): Cody-Waite
 // range reduction (W. J. Cody and W. Waite, "Software Manual for the Elementary Functions",
 // 1980) to f in [-1/2, 1/2], a degree-5 polynomial fitted for least largest relative error
-// there (7.5e-8), the integer part added to the exponent field.
+// there, the integer part added to the exponent field. Relative error with these fp32
+// coefficients and fp32 steps: 2.2e-7.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -83,7 +84,8 @@ __device__ __forceinline__ unsigned long long exp2_poly2(unsigned long long y) {
 }
 
 // tanh on the FMA pipes for |y| <= 1/2: an odd polynomial fitted for least largest error of
-// tanh(y)/y on that range (1.3e-8; 2^-24 absolute with its fp32 roundings).
+// tanh(y)/y on that range. With these fp32 coefficients and fp32 steps: relative error 1.2e-7,
+// absolute 4.4e-8.
 constexpr float kTanhPolyLimit = 0.5f;
 __device__ __forceinline__ unsigned long long tanh_poly2(unsigned long long y) {
   const unsigned long long z = f2_mul(y, y);
