@@ -625,8 +625,8 @@ typedef struct {
   const int32_t *cu_q, *cu_k;  /* device [n_docs + 1]               */
   const int32_t* prefix;       /* device [n_docs] (>= 0) or NULL: 0 */
   int causal_block;            /* >= 0                              */
-  float scale;                 /* finite; 0: 1/sqrt(head_dim)       */
-  float cap;                   /* finite, >= 0                      */
+  float scale;                 /* 0: 1/sqrt(head_dim); |scale| < 2^127                       */
+  float cap;                   /* >= 0, < 2^127; above 0: 2^-126 <= |scale| / cap < 2^128    */
   const float* slopes;         /* device [heads] fp32 or NULL       */
 } wan_documents;
 

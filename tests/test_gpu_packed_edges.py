@@ -130,3 +130,23 @@ def test_residual_norm_gradient_of_nothing(wan, rows, n_docs):
     before = wan.launch_count()
     wan.gated_residual_norm_bwd(cfg, spec, x, y, e, mb, cu, x, None, dx, dy, ws)
     assert wan.launch_count() == before
+
+
+def test_extreme_caps(wan):
+    """A cap far above all scores is none; one far below them leaves every key alike, and no
+    gradient but the values'."""
+    H, d, n = 2, 128, 150
+    g = _gen(6)
+    q, k, v, do = (torch.randn(n, H * d, generator=g, device="cuda").bfloat16() for _ in range(4))
+    q[5] = 0  # scores of 0
+    cfg, cu = wan.make_config(H * d, H, 64), _i32([0, n])
+    want = R.attention(*(t.double() for t in (q, k, v)), H, H, [0, n], [0, n], torch.bfloat16, do=do.double())
+    got = _attention(wan, cfg, wan.documents(cu, cap=1e30), q, k, v, H, do=do)
+    for name in got:
+        R.assert_close(got[name], *want[name], name)
+    got = _attention(wan, cfg, wan.documents(cu, cap=1e-30), q, k, v, H, do=do)
+    want = R.attention(*(t.double() for t in (q, k, v)), H, H, [0, n], [0, n], torch.bfloat16, do=do.double(), cap=1e-30)
+    for name in ("o", "lse", "dv"):
+        R.assert_close(got[name], *want[name], name)
+    others = torch.arange(n, device="cuda") != 5
+    assert not got["dq"][others].any() and torch.isfinite(got["dq"]).all() and torch.isfinite(got["dk"]).all()

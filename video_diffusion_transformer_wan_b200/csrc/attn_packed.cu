@@ -1,5 +1,6 @@
 // The C entry points of the attention inside packed documents: argument checks, workspace
 // layout and the choice of kernel (fp32: the CUDA cores; bf16: the tensor cores).
+#include <float.h>
 #include <math.h>
 
 #include "checks.h"
@@ -8,6 +9,20 @@
 namespace wan {
 namespace {
 
+float score_scale(const wan_dit_config* cfg, const wan_documents* d) {
+  return d->scale != 0.f ? d->scale : static_cast<float>(1.0 / sqrt(static_cast<double>(cfg->head_dim)));
+}
+
+// The factors that the kernels work with are numbers: a score in log2 units and, with a cap, the
+// argument of its tanh (an infinite factor would make NaN of a score of 0, a subnormal one
+// loses its digits).
+int check_factors(float scale, float cap) {
+  const float log2e = 1.4426950408889634f, in = cap > 0.f ? fabsf(scale / cap) : 1.f;
+  WAN_REQUIRE(isfinite(scale * log2e) && isfinite(cap * log2e), WAN_ERR_SHAPE);
+  WAN_REQUIRE(isfinite(in) && in >= FLT_MIN, WAN_ERR_SHAPE);
+  return WAN_OK;
+}
+
 int check_docs(const wan_dit_config* cfg, const wan_documents* d, int q_rows, int k_rows, int kv_heads) {
   WAN_TRY(check_cfg(cfg, true));
   WAN_REQUIRE(d, WAN_ERR_NULL);
@@ -15,6 +30,7 @@ int check_docs(const wan_dit_config* cfg, const wan_documents* d, int q_rows, in
   WAN_REQUIRE(kv_heads >= 1 && cfg->heads % kv_heads == 0 && cfg->heads <= 65535, WAN_ERR_SHAPE);
   WAN_REQUIRE(d->causal_block >= 0, WAN_ERR_SHAPE);
   WAN_REQUIRE(isfinite(d->scale) && isfinite(d->cap) && d->cap >= 0.f, WAN_ERR_SHAPE);
+  WAN_TRY(check_factors(score_scale(cfg, d), d->cap));
   WAN_TRY(check_ints(d->cu_q, d->n_docs + 1));
   WAN_TRY(check_ints(d->cu_k, d->n_docs + 1));
   WAN_TRY(check_opt_ptr(d->prefix));
@@ -28,7 +44,7 @@ PackedAttn make_packed(const wan_dit_config* cfg, const wan_documents* d, int q_
   p.cu_q = d->cu_q, p.cu_k = d->cu_k, p.prefix = d->prefix, p.slopes = d->slopes;
   p.n_docs = d->n_docs, p.q_rows = q_rows, p.k_rows = k_rows;
   p.H = cfg->heads, p.Hk = kv_heads, p.d = cfg->head_dim, p.causal_block = d->causal_block;
-  p.scale = d->scale != 0.f ? d->scale : static_cast<float>(1.0 / sqrt(static_cast<double>(cfg->head_dim)));
+  p.scale = score_scale(cfg, d);
   p.cap = d->cap;
   p.q = q->ptr, p.k = k->ptr, p.v = v->ptr, p.o = o->ptr;
   p.q_stride = q->row_stride, p.k_stride = k->row_stride, p.v_stride = v->row_stride, p.o_stride = o->row_stride;
