@@ -150,3 +150,101 @@ def test_extreme_caps(wan):
         R.assert_close(got[name], *want[name], name)
     others = torch.arange(n, device="cuda") != 5
     assert not got["dq"][others].any() and torch.isfinite(got["dq"]).all() and torch.isfinite(got["dk"]).all()
+
+
+def _against_reference(wan, dtype, d, H, Hk, q_lens, k_lens, seed, split=True, first=0, spare=0, grads=True, k_growth=None, **opt):
+    """One call (and its gradient) against the 64-bit form; returns what the call wrote."""
+    act, g, opt = ACT[dtype], _gen(seed), dict(opt)
+    nq, nk = first + sum(q_lens) + spare, first + sum(k_lens) + spare
+    q, do = (torch.randn(nq, H * d, generator=g, device="cuda") for _ in range(2))
+    k, v = (torch.randn(nk, Hk * d, generator=g, device="cuda") for _ in range(2))
+    if k_growth:
+        k *= torch.linspace(*k_growth, nk, device="cuda")[:, None]
+    q, k, v, do = (t.to(act) for t in (q, k, v, do))
+    slopes = [2.0 ** (-8.0 * (h + 1) / H) for h in range(H)] if opt.pop("slopes", False) else None
+    cu_q, cu_k = R.cu_of(q_lens, first), R.cu_of(k_lens, first)
+    scale = opt.get("scale", 0.0)
+    docs = wan.documents(_i32(cu_q), _i32(cu_k), prefix=_i32(opt["prefix"]) if opt.get("prefix") else None,
+                         causal_block=opt.get("block", 0), cap=opt.get("cap", 0.0), scale=scale,
+                         slopes=None if slopes is None else torch.tensor(slopes, device="cuda"))
+    cfg = wan.make_config(H * d, H, 64, dtype=dtype)
+    got = _attention(wan, cfg, docs, q, k, v, Hk, do=do if grads else None, split=split)
+    # a negative scale is a positive one with -q, and -dq
+    flip = -1.0 if scale < 0 else 1.0
+    opt["scale"] = abs(scale)
+    want = R.attention(flip * q.double(), k.double(), v.double(), H, Hk, cu_q, cu_k, act, do=do.double() if grads else None,
+                       slopes=slopes, **opt)
+    for name in got:
+        R.assert_close(flip * got[name].double() if name == "dq" else got[name], *want[name], name,
+                       untouched=flip * 7.0 if name == "dq" else 7.0)
+    return got
+
+
+@pytest.mark.parametrize("d,H,Hk", [(4, 16, 4), (32, 4, 2), (60, 16, 16), (68, 16, 8), (96, 2, 1), (128, 3, 1), (128, 2, 2)])
+@pytest.mark.parametrize("case", [([60, 0, 33], [50, 7, 70], dict()), ([100, 1], [100, 1], dict(block=1, slopes=True)),
+                                  ([37, 20], [37, 20], dict(block=8, prefix=[9, 0], cap=4.0)), ([3], [300], dict(block=1, cap=15.0, slopes=True))],
+                         ids=["texts", "causal", "frames", "step"])
+def test_float32_head_dims(wan, d, H, Hk, case):
+    q_lens, k_lens, opt = case
+    _against_reference(wan, "f32", d, H, Hk, q_lens, k_lens, seed=d + H, first=2, spare=3, **opt)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64), ("f32", 128)])
+@pytest.mark.parametrize("opt", [dict(), dict(cap=2.0), dict(slopes=True), dict(cap=2.0, slopes=True, block=1)],
+                         ids=["plain", "cap", "slopes", "all"])
+def test_negative_scale(wan, dtype, d, opt):
+    _against_reference(wan, dtype, d, 4, 2, [70, 200], [70, 200], seed=3, scale=-0.11, **opt)
+
+
+def _cut_pieces(H, Hk, lq, lk, block):
+    """The forward's shares of one document in causal blocks (no waves): for every piece of a cut
+    unit, the key tiles that its two query tiles have in it."""
+    group = H // Hk
+    pack = max(n for n in range(1, 129) if group % n == 0)
+    per_tile, ctas = 128 // pack, torch.cuda.get_device_properties(0).multi_processor_count
+
+    def tiles(first, rows):
+        if first >= lq:
+            return 0
+        pos = min(first + rows, lq) - 1 + lk - lq
+        return -(-max(0, min(lk, (pos // block + 1) * block if pos >= 0 else 0)) // 128)
+
+    units = [max(1, tiles(u, 2 * per_tile)) for u in range(0, lq, 2 * per_tile)] * (H // pack)
+    firsts = list(range(0, lq, 2 * per_tile)) * (H // pack)
+    total = sum(n + 2 for n in units)
+    share = max(1, min(ctas, total // 4))
+    at, out = 0, []
+    for n, f in zip(units, firsts):
+        ends = {total * c // share for c in range(share + 1)}
+        cuts = [0] + sorted(e - at for e in ends if 0 < e - at < n) + [n]
+        if n > 8 and len(cuts) > 2:
+            for a, b in zip(cuts, cuts[1:]):
+                out.append([max(0, min(tiles(f + t * per_tile, per_tile), b) - a) for t in range(2)])
+        at += n + 2
+    return out
+
+
+@pytest.mark.parametrize("H,Hk,lq,lk,block,opt", [
+    (2, 2, 700, 2600, 128, dict()), (4, 2, 515, 3100, 1, dict(cap=15.0)), (6, 2, 900, 1800, 300, dict(slopes=True)),
+    (3, 3, 1300, 1300, 64, dict(prefix=[40], cap=30.0, slopes=True)), (2, 1, 1500, 1200, 50, dict())])
+def test_units_cut_under_an_order_mask(wan, H, Hk, lq, lk, block, opt):
+    pieces = _cut_pieces(H, Hk, lq, lk, block)
+    assert len(pieces) > 4
+    if (H, lq) in ((2, 700), (4, 515)):
+        assert any(a == 0 and b > 0 for a, b in pieces)  # keys that only the second query tile sees
+    _against_reference(wan, "bf16", 128, H, Hk, [lq], [lk], seed=lq, block=block, grads=False, spare=3, **opt)
+
+
+@pytest.mark.parametrize("growth", [(0.1, 8.0), (8.0, 0.1)])
+@pytest.mark.parametrize("lq,H,Hk,opt", [(200, 2, 2, dict()), (300, 4, 2, dict(block=32)), (1, 6, 2, dict(block=1)),
+                                         (2, 8, 1, dict(slopes=True))])
+def test_scores_that_grow_through_cut_units(wan, growth, lq, H, Hk, opt):
+    """The base of the exponentials moves inside the parts and differs between them."""
+    cut = _against_reference(wan, "bf16", 128, H, Hk, [lq], [4000], seed=8, grads=False, k_growth=growth, **opt)
+    whole = _against_reference(wan, "bf16", 128, H, Hk, [lq], [4000], seed=8, grads=False, k_growth=growth, split=False, **opt)
+    assert any(not torch.equal(cut[name], whole[name]) for name in cut)  # other sums, of the same value
+
+
+def test_capped_scores_and_their_gradient_on_both_sides_of_half_the_cap(wan):
+    for cap in (1.0, 3.0, 400.0):
+        _against_reference(wan, "bf16", 128, 4, 2, [300, 45], [300, 45], seed=5, block=1, cap=cap, scale=1.0)
