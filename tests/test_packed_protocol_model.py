@@ -444,3 +444,24 @@ def test_keys_gradient(n):
 def test_forward(pieces):
     for seed in range(30):
         assert run_forward(pieces, seed)
+
+
+def test_float32_blocks_wait_for_copies_of_no_group():
+    """A block whose rows see nothing (or no query sees its keys) copies its own rows and commits no
+    group; what it waits for before it leaves has to cover those copies."""
+    text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, "attn_packed_simt.cu")).read())
+    wait_all = re.search(r'void async_wait_all\(\) \{ asm volatile\("([^"]*)"', text).group(1)
+    kernels = re.findall(r"packed_(?:fwd|dq|dkv)_kernel\(const PackedAttn p\) \{(.*?)\n\}", text, re.S)
+    assert len(kernels) == 3
+    for kernel in kernels:
+        copies = len(re.findall(r"\n  load_async<D>\(s[qkov],", kernel))
+        assert copies > 0
+        pending = 0  # copies not waited for where the walk has no tile
+        for line in (kernel[:kernel.index("st ^= 1) {")] + kernel[kernel.rindex("async_wait_all();"):]).splitlines():
+            if "auto load" in line or "if (most > 0) load" in line or "if (n > 0) load" in line:
+                continue
+            if re.match(r"\s{2}load_async<D>\(s[qkov],", line):
+                pending += 1
+            if "async_wait_all();" in line and wait_all == "cp.async.wait_all;":
+                pending = 0
+        assert pending == 0

@@ -58,7 +58,10 @@ __device__ __forceinline__ void load_async(float* dst, const void* src, int64_t 
   }
 }
 __device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void async_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void async_wait_groups() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+// Those of no group too: a block without a tile of the other side commits none, and leaves
+// only when its own rows have landed.
+__device__ __forceinline__ void async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // s[i][j] = row (2 ty + i) of a . row (tx + 16 j) of b.
 template <int D>
@@ -160,7 +163,7 @@ __global__ void __launch_bounds__(kThreads) packed_fwd_kernel(const PackedAttn p
   for (int i = 0; i < 2; ++i)
     seen[i] = 2 * ty + i < rows ? seen_keys(i0 + 2 * ty + i, doc.off, doc.Lk, doc.prefix, p.causal_block) : 0;
   for (int j0 = 0, st = 0; j0 < most; j0 += kC, st ^= 1) {
-    async_wait_all();
+    async_wait_groups();
     __syncthreads();  // this tile is there; the other stage has been read
     if (j0 + kC < most) load(j0 + kC, st ^ 1);
     float s[2][2];
@@ -245,7 +248,7 @@ __global__ void __launch_bounds__(kThreads) packed_dq_kernel(const PackedAttn p)
   }
   float4 g[2][D / 64] = {};
   for (int j0 = 0, st = 0; j0 < most; j0 += kC, st ^= 1) {
-    async_wait_all();
+    async_wait_groups();
     __syncthreads();
     if (j0 + kC < most) load(j0 + kC, st ^ 1);
     float s[2][2], dp[2][2];
@@ -311,7 +314,7 @@ __global__ void __launch_bounds__(kThreads) packed_dkv_kernel(const PackedAttn p
         lse[x] = p.lse[stat], delta[x] = p.delta[stat];
       }
     }
-    async_wait_all();
+    async_wait_groups();
     __syncthreads();
     if (t + 1 < n) load(t + 1, st ^ 1);
     float s[2][2], dp[2][2];
