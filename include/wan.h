@@ -497,16 +497,16 @@ size_t wan_attention_fp8_workspace_bytes(const wan_dit_config* cfg, int B, int L
 /* A packed tensor holds documents (clips, images, texts) of different lengths one after
  * another along its row axis: document d of n_docs owns rows [cu[d], cu[d+1]) of a
  * DEVICE array cu of n_docs + 1 int32, 0 <= cu[0] <= cu[1] <= ... <= the tensor's rows
- * (offsets outside that order are clamped into it, so they cannot reach past the
- * tensor). A document may be empty. Rows in front of cu[0] and from cu[n_docs] on belong
+ * (offsets outside that order are clamped: they reach no row outside the tensor, but which
+ * rows of it are written, and with what, is not specified then). A document may be empty. Rows in front of cu[0] and from cu[n_docs] on belong
  * to no document: the calls neither use their values nor write their results. The Wan 2.1
  * pages have no counterpart of these calls (their batches share one length, and the pages
  * name neither positions nor a q/k norm); they are the parts that a model with them, or a
  * batch of clips of mixed sizes, needs beside wan_adaln_modulate, wan_linear_fwd and
  * wan_attention_fwd, with their gradients. Tensors of one call must not overlap unless a
  * call says so. Offsets are 64-bit: a tensor may exceed 2^31 elements; row counts are int.
- * Arrays of offsets and positions need 4-byte alignment only (a slice of one will do). A
- * workspace serves one call at a time: calls that may overlap (two streams) need one each.
+ * Arrays of offsets and positions need 4-byte alignment only (a slice of one will do); every
+ * other pointer, prefix and slopes included, 16-byte. A workspace serves one call at a time: calls that may overlap (two streams) need one each.
  * All results are the same from run to run (no atomics on floating-point values). */
 
 /* Rows of a tensor: row r starts at ptr + r * row_stride elements. ptr is 16-byte
@@ -632,8 +632,9 @@ typedef struct {
 
 /* q [q_rows, heads*head_dim], k and v [k_rows, kv_heads*head_dim] act -> o [q_rows,
  * heads*head_dim] act and, unless NULL, lse [heads, q_rows] fp32 (natural log of the sum of
- * e^s). kv_heads divides heads. Values of a document's own rows must be finite. The
- * workspace lets few query rows over many keys be split over the keys; it may be NULL
+ * e^s). kv_heads divides heads. Values of a document's own rows must be finite. In bf16 the
+ * probabilities are rounded to bf16 before their product with v (the tensor cores' operand), as
+ * are, in the gradient, p and ds before theirs; scores, sums and statistics are fp32. The workspace lets few query rows over many keys be split over the keys; it may be NULL
  * (0 bytes), which never splits. */
 int wan_attention_packed_fwd(const wan_dit_config* cfg, const wan_documents* docs, int q_rows, int k_rows,
                              int kv_heads, const wan_rows* q, const wan_rows* k, const wan_rows* v, const wan_rows* o,
