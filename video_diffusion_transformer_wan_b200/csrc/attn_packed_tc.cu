@@ -20,7 +20,7 @@
 //              exponentials moves only when the row maximum grew by more than 2^8.
 // While one tile's softmax runs, the tensor core works on the other's products. What bounds it
 // is that chain: about 3,300 clocks per key tile for 2,048 of tensor work and as many of
-// exponentials. 4 clips of 23,400 rows, 12 heads: 1.37 ms, 1080 TFLOP/s under the power cap; 8
+// exponentials. 4 clips of 23,400 rows, 12 heads: 1.36 to 1.38 ms, 1080 TFLOP/s under the power cap; 8
 // single tokens over 117 k keys, 12/4 heads: 71 us, 3.4 TB/s.
 //
 // Whole waves of equal units (a document's, as many as there are CTAs) come first. What they
@@ -326,7 +326,8 @@ __device__ __forceinline__ int pos_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
 __device__ __forceinline__ int pos_v(int j, int n) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; }
 
 // kPlain: scores are neither capped nor scaled before their maximum. The passes for those
-// cost registers even where a call skips them (the plain loop then spilled).
+// cost registers even where a call skips them (each instance spills a little: 4 bytes the plain
+// one, 12 the other).
 template <bool kPlain>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_fwd_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,

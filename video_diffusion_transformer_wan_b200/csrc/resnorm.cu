@@ -19,8 +19,8 @@
 // collide), and are added in order by a second kernel: no atomics. Statistics are fp32, squares
 // about a mean (the row's, or, in the gradient, the warp's and then moved). What bounds them
 // now are the barriers and the latencies between them: forward 124 us for 604 MB (4.9 TB/s,
-// 32,760 rows of 1536; a block's rows consecutive, 134 us with rows dealt out in turn), gradient 545 us for 2.07 GB (3.8 TB/s, 22,501 rows of 5120; 1263 us
-// with five barriers a row and the sums in registers).
+// 32,760 rows of 1536; a block's rows consecutive, 134 us with rows dealt out in turn), gradient 552 to 562 us (three cards) for 2.07 GB (3.7 TB/s, 22,501 rows of 5120;
+// 1263 us with five barriers a row and the sums in registers).
 #include <cuda_bf16.h>
 
 #include "checks.h"
@@ -276,7 +276,9 @@ __device__ __forceinline__ void sm_put(float4* sm, int which, const F2 (&v)[4]) 
 size_t bwd_smem(int threads, int nu) { return static_cast<size_t>(threads) * nu * 5 * 32; }
 
 // The document's vectors (gate w_post, w (1 + scale)) and the three column sums live in shared
-// memory: in registers they left room for one block an SM, or spilled.
+// memory: in registers they left room for one block an SM, or spilled more. (Two blocks of 320 threads
+// have 96 registers a thread; at widths from 2049 to 5120 that still spills 84 bytes in bf16, 220 in
+// fp32.)
 template <typename T, int NU, int kMaxThreads, int kMinBlocks>
 __global__ void __launch_bounds__(kMaxThreads, kMinBlocks) gated_residual_norm_bwd_kernel(const ResNormParams p) {
   extern __shared__ float4 vec[];  // per unit: g, sc, s0, s1, s2

@@ -262,7 +262,11 @@ using F2 = unsigned long long;  // two fp32
 
 constexpr int kMaxHeads = 96;  // q and k heads of one row together
 constexpr int kWarps = 8;      // per block
-constexpr int kHeld = 6;       // groups of 256 columns that stay in registers
+// Groups of 256 columns that stay in registers. The gradient, 20,000 rows of 12 + 12 heads of 128:
+// held 116 us in bf16 and 181 in fp32 (which spills 80 to 92 bytes), read twice 219 and 299. Beyond 6
+// it reads twice, with one block an SM for its sums: 390 us for 20 + 20 heads and 876 for 40 + 40
+// (the general kernel 1940 and 3801), 4.2 and 4.7 times the bytes' time, against 2.1 at 12 + 12.
+constexpr int kHeld = 6;
 // More of them in the forward (read twice: 143, 161 and 268 us for 20, 24 and 40 heads of q and
 // of k on 20,000 rows; held: 98, 106 and 153), the last only of two bytes each.
 constexpr int kHeldMore = 12, kHeldMost = 20;
@@ -776,7 +780,8 @@ int run_rope(const wan_dit_config* cfg, RopeParams& p, bool vec, bool dw, RopePl
 
 // Every lane has whole groups of 8 dims at one place of every head (the head divides 256 dims,
 // split halves are whole quads), and the block's sums fit into shared memory (sides of up to
-// 6144 dims; any for the forward).
+// 6144 dims, where the gradient takes 1108 us on 20,000 rows and the general kernel 4523; any for
+// the forward).
 bool wide_fit(const wan_rope* r, const RopeParams& p, bool bwd) {
   if (p.d < 8 || 256 % p.d != 0 || (r->layout == WAN_ROPE_HALF && p.pairs % 4 != 0)) return false;
   return vec_smem(p, bwd) <= kMostSmem;
